@@ -22,7 +22,9 @@ VARIANT_AUTO, VARIANT_SIMT, VARIANT_TC, VARIANT_TC8, VARIANT_W8A8, VARIANT_PRESP
     0, 1, 2, 3, 4, 5, 6)
 VARIANT_STREAM = 7
 STATUS_OK, STATUS_WAIT_TIMEOUT = 0, 1
+STATUS_BAD_INDEX = 2
 WEIGHTS_F32, WEIGHTS_BF16 = 0, 1
+ACT_BF16, ACT_F16 = 0, 1
 
 
 class Plan(ctypes.Structure):
@@ -39,6 +41,32 @@ class Plan(ctypes.Structure):
                 "block": list(self.block), "cluster": list(self.cluster),
                 "smem_bytes": self.smem_bytes, "tmem_cols": self.tmem_cols,
                 "tail_tiles": self.tail_tiles, "tail_split": self.tail_split}
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("num_pages", ctypes.c_uint32),
+                ("page_size", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("page_table_stride", ctypes.c_int64), ("max_pages", ctypes.c_uint32),
+                ("batch", ctypes.c_uint32), ("tokens", ctypes.c_uint32), ("max_q", ctypes.c_uint32)]
+
+
+class HeadsDesc(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_uint32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_uint32),
+                ("rotary_dim", ctypes.c_uint32), ("interleaved", ctypes.c_uint32)]
 
 
 class W8A16Error(RuntimeError):
@@ -77,6 +105,8 @@ _SIGS = {
                                _VP]),
     "w8a16_gemm_w8a8_with_plan": (_INT, [_VP, _U32, _VP, _U32, _VP, _VP, _VP, _U32, _U32, _U32,
                                          _U32, ctypes.POINTER(Plan), _U32, _VP]),
+    "w8a16_kv_append": (_INT, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _U32]
+                        + [ctypes.POINTER(HeadsDesc)] * 4 + [ctypes.POINTER(RopeDesc), _VP]),
     "w8a16_last_error": (ctypes.c_char_p, []),
     "w8a16_strerror": (ctypes.c_char_p, [_INT]),
     "w8a16_device_status": (_INT, [_VP, _INT, ctypes.POINTER(_U32), ctypes.POINTER(_U32),
@@ -505,6 +535,148 @@ def quantize_weights_ptr(W_ptr, w_dtype, w_row_stride, N, K, codes_ptr, scale_pt
     """Raw-pointer call (returns the library's code; does not raise)."""
     return load().w8a16_quantize_weights(W_ptr or None, w_dtype, w_row_stride, N, K, codes_ptr or None,
                                          scale_ptr or None, stream or None)
+
+
+# ------------------------------------------------- 8-bit paged key/value cache --
+def _act_type(t, name) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return ACT_BF16
+    if t.dtype is torch.float16:
+        return ACT_F16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _device_call(index, stream, fn, *args):
+    """fn(*args, stream handle) on CUDA device `index` (stream None: its current one)."""
+    import torch
+    if index == torch.cuda.current_device():
+        if stream is None:
+            return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        return fn(*args, _stream_handle(stream))
+    with torch.cuda.device(index):
+        return fn(*args, _stream_handle(stream))
+
+
+def _same_gpu(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one CUDA device (cuda:{index}; got {t.device})")
+
+
+class KVCache:
+    """A paged key/value cache in E4M3 with one float32 scale per page and head.
+
+    k_codes, v_codes: uint8 or float8_e4m3fn [pages, kv_heads, page_size, head_dim] views
+    with unit stride along head_dim and the same strides (a [pages, page_size, kv_heads,
+    head_dim] pool is passed as its .transpose(1, 2)); k_scale, v_scale: float32
+    [pages, kv_heads]. page_size a power of two in 16..256, head_dim a multiple of 16
+    up to 256. The tensors are the caller's and are kept alive by the object."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        import torch
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            if t.dim() != 4 or not _is_codes(t) or t.stride(3) != 1:
+                raise ValueError(f"{name} must be E4M3 codes [pages, kv_heads, page_size, head_dim] "
+                                 "(uint8 or float8_e4m3fn) with unit stride along head_dim")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or tuple(t.shape) != tuple(k_codes.shape[:2]):
+                raise ValueError(f"{name} must be float32 {list(k_codes.shape[:2])}")
+        if k_codes.shape != v_codes.shape or k_codes.stride() != v_codes.stride():
+            raise ValueError("k_codes and v_codes must have the same shape and strides")
+        if k_scale.stride() != v_scale.stride():
+            raise ValueError("k_scale and v_scale must have the same strides")
+        _on_one_gpu(k_codes, v_codes, k_scale, v_scale)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_codes.shape
+        self._index = k_codes.get_device()
+        self._desc = KvCacheDesc(
+            k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            k_codes.stride(0), k_codes.stride(1), k_codes.stride(2), k_scale.stride(0), k_scale.stride(1),
+            self.num_pages, self.page_size, self.kv_heads, self.head_dim)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, device="cuda"):
+        """A cache of zeroed pages [pages, kv_heads, page_size, head_dim]."""
+        import torch
+        kv = [torch.zeros(num_pages, kv_heads, page_size, head_dim, dtype=torch.uint8, device=device)
+              for _ in range(2)]
+        sc = [torch.zeros(num_pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*kv, *sc)
+
+
+def _kv_batch(cache, rows, page_table, lens, cu_q, max_q) -> KvBatchDesc:
+    import torch
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [batch, max_pages] with contiguous rows")
+    B, max_pages = page_table.shape
+    if lens.dtype is not torch.int32 or lens.dim() != 1 or lens.shape[0] != B or not lens.is_contiguous():
+        raise ValueError(f"lens must be contiguous int32 [{B}]")
+    if cu_q is None:
+        if max_q is None:
+            if B == 0 or rows % B:
+                raise ValueError(f"{rows} rows do not divide among {B} sequences: pass cu_q and max_q")
+            max_q = rows // B
+    else:
+        if cu_q.dtype is not torch.int32 or cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
+            raise ValueError(f"cu_q must be contiguous int32 [{B + 1}]")
+        if max_q is None:
+            raise ValueError("cu_q needs max_q, the most rows of one sequence")
+    _same_gpu(cache._index, page_table, lens, cu_q)
+    return KvBatchDesc(page_table.data_ptr(), lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(),
+                       page_table.stride(0), max_pages, B, rows, max_q)
+
+
+def _heads(cache, t, name, rows, dtype) -> HeadsDesc:
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [{rows}, heads, {cache.head_dim}] with unit stride along the head; "
+                         f"got {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} like the others, got {t.dtype}")
+    return HeadsDesc(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+
+
+def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_out=None, cu_q=None, max_q=None,
+              interleaved=False, stream=None):
+    """w8a16_kv_append: writes this call's keys (rotated) and values to the cache, and
+    returns the rotated queries.
+
+    k, v: bf16 or fp16 [tokens, kv_heads, head_dim] (any token and head strides that are
+    multiples of 8); q: [tokens, heads, head_dim] or None; q_out: where the rotated
+    queries go (None: a new tensor; may be q itself). page_table: int32
+    [batch, max_pages]; lens: int32 [batch], each sequence's length with the call's
+    tokens, which are its last ones. Rows are split evenly among the sequences, or by
+    cu_q (int32 [batch + 1] offsets) with max_q the most rows of one. cos, sin: float32
+    [positions, rotary_dim / 2], rotary_dim a multiple of 16 up to head_dim (None: no
+    rotation); pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved."""
+    import torch
+    rows = k.shape[0]
+    act = _act_type(k, "k")
+    batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
+    kd, vd = _heads(cache, k, "k", rows, k.dtype), _heads(cache, v, "v", rows, k.dtype)
+    qd = od = None
+    if q is not None:
+        qd = _heads(cache, q, "q", rows, k.dtype)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        od = _heads(cache, q_out, "q_out", rows, k.dtype)
+        qd_ref, od_ref = ctypes.byref(qd), ctypes.byref(od)
+    else:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        qd_ref = od_ref = None
+    if cos is None:
+        rope = RopeDesc(None, None, 0, 0, 0)
+    else:
+        if (sin is None or cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not torch.float32
+                or sin.dtype is not torch.float32 or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous float32 [positions, rotary_dim / 2]")
+        rope = RopeDesc(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], 1 if interleaved else 0)
+    _same_gpu(cache._index, k, v, q, q_out, cos, sin)
+    _check(_device_call(cache._index, stream, load().w8a16_kv_append, cache._ref, ctypes.byref(batch), act,
+                        ctypes.byref(kd), ctypes.byref(vd), qd_ref, od_ref, ctypes.byref(rope)))
+    return q_out
 
 
 def device_status(stream=None, clear=False) -> tuple[int, int, int]:

@@ -856,6 +856,19 @@ int run_w8a8(const w8a16::W8A8Args& g, const w8a16_plan_t* forced, uint32_t flag
 
 }  // namespace
 
+namespace w8a16 {
+int api_fail(int code, const std::string& msg) { return fail(code, msg); }
+int api_ok() { return ok(); }
+int api_device(int* sm_count) {
+    DeviceInfo info;
+    std::string err;
+    const int rc = current_device_info(&info, &err);
+    if (rc) return fail(rc, err);
+    *sm_count = info.sm_count;
+    return W8A16_OK;
+}
+}  // namespace w8a16
+
 extern "C" {
 
 int w8a16_check_args(const void* A, uint32_t a_row_stride, const void* W, const float* block_scale,
@@ -1248,9 +1261,13 @@ int w8a16_device_status(w8a16_stream_t stream, int clear, uint32_t* status, uint
         e = w8a16::w8a8_status_read(&wa, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess)
         e = w8a16::gemv_status_read(&wg, clear != 0, reinterpret_cast<cudaStream_t>(stream));
+    w8a16::StatusWord wk{0, 0, 0};
+    if (e == cudaSuccess)
+        e = w8a16::kv_append_status_read(&wk, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (w.code == 0) w = w8;
     if (w.code == 0) w = wa;
     if (w.code == 0) w = wg;
+    if (w.code == 0) w = wk;
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(W8A16_ERR_DEVICE, std::string("w8a16_device_status: ") + cudaGetErrorString(e));

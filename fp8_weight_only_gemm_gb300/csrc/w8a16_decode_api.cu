@@ -1,0 +1,132 @@
+// C entries of the decode-step operators around the GEMM: the paged 8-bit cache's
+// append and attention. All checks run on the host before any device work;
+// what only device memory tells (lengths, page numbers) the kernels check.
+#include <cuda_runtime.h>
+
+#include <new>
+#include <string>
+
+#include "w8a16_internal.h"
+
+namespace {
+
+using w8a16::api_fail;
+using w8a16::api_ok;
+
+std::string u(uint64_t v) { return std::to_string(v); }
+bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// No C++ exception leaves a C entry: the messages allocate.
+template <typename F>
+int guarded(F&& f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return W8A16_ERR_ARG;
+    }
+}
+
+int check_act(const char* who, uint32_t act_dtype) {
+    if (act_dtype != W8A16_ACT_BF16 && act_dtype != W8A16_ACT_F16)
+        return api_fail(W8A16_ERR_ARG, std::string(who) + ": unknown activation type " + u(act_dtype));
+    return W8A16_OK;
+}
+
+int check_cache(const char* who, const w8a16_kv_cache_t* c) {
+    const std::string w(who);
+    if (!c) return api_fail(W8A16_ERR_NULL, w + ": NULL cache");
+    if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale)
+        return api_fail(W8A16_ERR_NULL, w + ": NULL cache pointer");
+    if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
+        return api_fail(W8A16_ERR_ARG, w + ": head_dim=" + u(c->head_dim) + " must be a multiple of 16 in 16..256");
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+        return api_fail(W8A16_ERR_ARG, w + ": page_size=" + u(c->page_size) + " must be a power of two in 16..256");
+    if (c->kv_heads < 1 || c->kv_heads > 65535)
+        return api_fail(W8A16_ERR_ARG, w + ": kv_heads=" + u(c->kv_heads) + " must be in 1..65535");
+    if (c->num_pages < 1 || c->num_pages > 0x7FFFFFFFu)
+        return api_fail(W8A16_ERR_RANGE, w + ": num_pages=" + u(c->num_pages) + " must be in 1..2^31-1");
+    if (misaligned(c->k_codes, 16) || misaligned(c->v_codes, 16) || misaligned(c->k_scale, 4) || misaligned(c->v_scale, 4))
+        return api_fail(W8A16_ERR_ALIGN, w + ": cache codes need 16-byte alignment, scales 4");
+    if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
+        return api_fail(W8A16_ERR_ALIGN, w + ": cache strides must be multiples of 16 bytes");
+    return W8A16_OK;
+}
+
+int check_batch(const char* who, const w8a16_kv_cache_t* c, const w8a16_kv_batch_t* b) {
+    const std::string w(who);
+    if (!b) return api_fail(W8A16_ERR_NULL, w + ": NULL batch");
+    if (b->batch < 1 || b->tokens < 1 || b->max_q < 1)
+        return api_fail(W8A16_ERR_M_ZERO, w + ": no sequences or tokens (batch=" + u(b->batch) + ", tokens=" + u(b->tokens) +
+                                              ", max_q=" + u(b->max_q) + ")");
+    if (!b->page_table || !b->lens) return api_fail(W8A16_ERR_NULL, w + ": NULL page_table or lens");
+    if (misaligned(b->page_table, 4) || misaligned(b->lens, 4) || misaligned(b->cu_q, 4))
+        return api_fail(W8A16_ERR_ALIGN, w + ": page_table, lens and cu_q need 4-byte alignment");
+    if (b->batch > 0x7FFFFFFFu || b->tokens > 0x7FFFFFFFu || b->max_q > b->tokens)
+        return api_fail(W8A16_ERR_RANGE, w + ": batch=" + u(b->batch) + ", tokens=" + u(b->tokens) +
+                                             " must be below 2^31 and max_q=" + u(b->max_q) + " at most tokens");
+    if (!b->cu_q && static_cast<uint64_t>(b->batch) * b->max_q != b->tokens)
+        return api_fail(W8A16_ERR_ARG, w + ": without cu_q, tokens=" + u(b->tokens) + " must be batch=" + u(b->batch) +
+                                           " times max_q=" + u(b->max_q));
+    if (b->max_pages < 1 || static_cast<uint64_t>(b->max_pages) * c->page_size > 0x7FFFFF00ull)
+        return api_fail(W8A16_ERR_RANGE, w + ": max_pages=" + u(b->max_pages) + " pages of " + u(c->page_size) +
+                                             " must hold 1..2^31-256 tokens");
+    return W8A16_OK;
+}
+
+int check_heads(const char* who, const char* name, const w8a16_heads_t* h, uint32_t heads) {
+    const std::string w = std::string(who) + ": " + name;
+    if (!h || !h->ptr) return api_fail(W8A16_ERR_NULL, w + " is NULL");
+    if (heads ? h->heads != heads : h->heads < 1 || h->heads > 1u << 20)
+        return api_fail(W8A16_ERR_ARG, w + " has " + u(h->heads) + " heads" + (heads ? ", not " + u(heads) : ""));
+    if (misaligned(h->ptr, 16) || h->token_stride % 8 || h->head_stride % 8)
+        return api_fail(W8A16_ERR_ALIGN, w + " needs 16-byte alignment and strides that are multiples of 8 elements");
+    return W8A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int w8a16_kv_append(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* batch, uint32_t act_dtype,
+                    const w8a16_heads_t* k, const w8a16_heads_t* v, const w8a16_heads_t* q, const w8a16_heads_t* q_out,
+                    const w8a16_rope_t* rope, w8a16_stream_t stream) {
+    return guarded([&] {
+        const char* who = "w8a16_kv_append";
+        int rc = check_cache(who, cache);
+        if (!rc) rc = check_batch(who, cache, batch);
+        if (!rc) rc = check_act(who, act_dtype);
+        if (!rc) rc = check_heads(who, "k", k, cache->kv_heads);
+        if (!rc) rc = check_heads(who, "v", v, cache->kv_heads);
+        if (rc) return rc;
+        w8a16_heads_t qi{}, qo{};
+        if (q && q->ptr) {
+            rc = check_heads(who, "q", q, 0);
+            if (!rc) rc = check_heads(who, "q_out", q_out, q->heads);
+            if (rc) return rc;
+            qi = *q;
+            qo = *q_out;
+        } else if (q_out && q_out->ptr) {
+            return api_fail(W8A16_ERR_NULL, std::string(who) + ": q_out without q");
+        }
+        if (!rope) return api_fail(W8A16_ERR_NULL, std::string(who) + ": NULL rope");
+        if (rope->rotary_dim % 16 || rope->rotary_dim > cache->head_dim)
+            return api_fail(W8A16_ERR_ARG, std::string(who) + ": rotary_dim=" + u(rope->rotary_dim) +
+                                               " must be a multiple of 16, at most head_dim=" + u(cache->head_dim));
+        if (rope->rotary_dim) {
+            if (!rope->cos || !rope->sin) return api_fail(W8A16_ERR_NULL, std::string(who) + ": NULL cos or sin");
+            if (misaligned(rope->cos, 16) || misaligned(rope->sin, 16))
+                return api_fail(W8A16_ERR_ALIGN, std::string(who) + ": cos and sin need 16-byte alignment");
+            if (rope->rows < 1 || rope->rows > 0x7FFFFFFFu)
+                return api_fail(W8A16_ERR_RANGE, std::string(who) + ": rope rows=" + u(rope->rows) + " must be in 1..2^31-1");
+        }
+        int sms = 0;
+        rc = w8a16::api_device(&sms);
+        if (rc) return rc;
+        std::string err;
+        rc = w8a16::launch_kv_append(*cache, *batch, act_dtype, *k, *v, qi, qo, *rope,
+                                     reinterpret_cast<cudaStream_t>(stream), &err);
+        return rc ? api_fail(rc, err) : api_ok();
+    });
+}
+
+}  // extern "C"

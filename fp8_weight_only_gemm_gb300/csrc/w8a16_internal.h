@@ -275,6 +275,20 @@ int launch_gemv_w8a8(const W8A8Args& a, const w8a16_plan_t& p, cudaStream_t s, u
 int gemv_cluster_capacity(uint32_t cluster, uint32_t* ctas, std::string* err);
 cudaError_t gemv_status_read(StatusWord* out, bool clear, cudaStream_t s);
 
+// ---- the paged cache (w8a16_kv_append.cu, w8a16_kv_attn.cu) ----
+// They assume checked arguments; the kernels check what only device memory tells
+// (page-table entries, lengths) and report it as W8A16_STATUS_BAD_INDEX.
+int launch_kv_append(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& k,
+                     const w8a16_heads_t& v, const w8a16_heads_t& q, const w8a16_heads_t& q_out,
+                     const w8a16_rope_t& rope, cudaStream_t s, std::string* err);
+cudaError_t kv_append_status_read(StatusWord* out, bool clear, cudaStream_t s);
+
+// Shared by the C entries of every translation unit (w8a16_api.cu): the last error's
+// message of this host thread, and the current device (sm_103 or an error).
+int api_fail(int code, const std::string& msg);
+int api_ok();
+int api_device(int* sm_count);
+
 // TMA descriptors of W ([N][K] E4M3, 128x128 boxes) and A ([M][K] BF16 at the
 // caller's pitch, 64 x token_tile boxes), 128-byte swizzle; cached per device.
 bool tc_tensor_map_w(const GemmArgs& g, int device, CUtensorMap* out, std::string* err);

@@ -74,7 +74,10 @@ enum {
 /* Device status words (w8a16_device_status). */
 enum {
     W8A16_STATUS_OK = 0,
-    W8A16_STATUS_WAIT_TIMEOUT = 1  /* a bounded in-kernel wait ran out; output undefined */
+    W8A16_STATUS_WAIT_TIMEOUT = 1, /* a bounded in-kernel wait ran out; output undefined */
+    W8A16_STATUS_BAD_INDEX = 2     /* a page-table entry, length or position outside its range
+                                      (w8a16_kv_append, w8a16_kv_attention): the access was
+                                      skipped; detail = the offending value */
 };
 
 /* Call flags (w8a16_gemm_ex). */
@@ -322,6 +325,90 @@ W8A16_API int w8a16_gemm_split_terms(const void *workspace, uint64_t workspace_b
                                      const float *block_scale, void *C, uint32_t c_row_stride,
                                      uint32_t M, uint32_t N, uint32_t K, uint32_t flags,
                                      w8a16_stream_t stream);
+
+/* ---- 8-bit paged key/value cache ----------------------------------------- */
+
+/* Element types of activations (A and C of w8a16_gemm_w4; q, k, v and the outputs
+ * of the cache calls). */
+enum {
+    W8A16_ACT_BF16 = 0,
+    W8A16_ACT_F16 = 1
+};
+
+/* A paged cache of E4M3 codes with one FP32 scale per page and head, for keys and
+ * for values alike: element (page, head, slot, d) of K is
+ *   e4m3(k_codes[page*page_stride + head*head_stride + slot*token_stride + d])
+ *       * k_scale[page*scale_page_stride + head*scale_head_stride].
+ * The strides are byte counts for the codes, element counts for the scales, and
+ * shared by K and V, so pages may be laid out [page][head][slot][d] or
+ * [page][slot][head][d]. Codes 16-byte aligned, code strides multiples of 16;
+ * page_size a power of two in 16..256; head_dim a multiple of 16 in 16..256. */
+typedef struct {
+    void *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride;
+    uint32_t num_pages, page_size, kv_heads, head_dim;
+} w8a16_kv_cache_t;
+
+/* The sequences of one call. Rows [cu_q[b], cu_q[b+1]) of q, k and v are sequence
+ * b's tokens of this call (cu_q NULL: max_q rows each, tokens = batch * max_q).
+ * lens[b] is the sequence's length with these tokens, which are its last ones: token
+ * t of T has position lens[b] - T + t. Tokens at negative positions (lens[b] < T)
+ * are padding: not written, and without attention. Position p lives in slot
+ * p % page_size of page page_table[b*page_table_stride + p/page_size]. Device
+ * memory but for the counts; max_q: the most rows of one sequence. */
+typedef struct {
+    const int32_t *page_table;
+    const int32_t *lens;
+    const int32_t *cu_q;
+    int64_t page_table_stride;
+    uint32_t max_pages, batch, tokens, max_q;
+} w8a16_kv_batch_t;
+
+/* Rows of heads: element (token, head, d) at ptr[token*token_stride +
+ * head*head_stride + d] (strides in elements, multiples of 8; ptr 16-byte aligned). */
+typedef struct {
+    void *ptr;
+    int64_t token_stride, head_stride;
+    uint32_t heads;
+} w8a16_heads_t;
+
+/* The rotary table: cos and sin FP32 [rows][rotary_dim/2] (16-byte aligned), row p
+ * for position p. The first rotary_dim (a multiple of 16, at most head_dim; 0 = no
+ * rotation, the pointers may then be NULL) elements of a head are rotated,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * on the pairs (i, i + rotary_dim/2), or (2i, 2i+1) with interleaved != 0. A table
+ * for long contexts (scaled positions or frequencies) is the caller's choice. */
+typedef struct {
+    const float *cos, *sin;
+    uint32_t rows, rotary_dim, interleaved;
+} w8a16_rope_t;
+
+/* w8a16_kv_append -- rotates the call's keys (and queries), and writes its keys and
+ * values to the cache.
+ *   k, v    [tokens][kv_heads][head_dim], BF16 or FP16 (act_dtype)
+ *   q       [tokens][heads][head_dim], rotated into q_out (which may be q); NULL with
+ *           q_out NULL to leave queries out
+ * The rotation is computed in FP32 (each product and sum rounded once); rotated
+ * queries are rounded once to the activation type, keys and values once to E4M3.
+ * Page scales: with amax the largest finite magnitude among a page's new values of
+ * one head, s = the smallest power of two with amax <= 448 s, at least 2^-60. A page
+ * whose first slot is written by the call takes s. In a page that already holds
+ * older tokens of the sequence the scale becomes max(old, s), and where it grows the
+ * older codes are rewritten for it (RNE of code * old/new: with powers of two only
+ * codes that fall below 2^-6 change value). Not-a-number and infinite values become
+ * the NaN code. The last page of a sequence must not be shared with another sequence
+ * of the call. Codes outside the sequences' slots are not touched.
+ * One kernel launch, queued as a programmatic dependent that waits for the previous
+ * kernel of the stream before it touches memory. Returns W8A16_OK once queued or a
+ * W8A16_ERR_* code (nothing queued). Page-table entries outside [0, num_pages),
+ * positions past the table's rows or past max_pages pages: skipped, reported by
+ * w8a16_device_status (W8A16_STATUS_BAD_INDEX). */
+W8A16_API int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_batch_t *batch,
+                              uint32_t act_dtype, const w8a16_heads_t *k, const w8a16_heads_t *v,
+                              const w8a16_heads_t *q, const w8a16_heads_t *q_out,
+                              const w8a16_rope_t *rope, w8a16_stream_t stream);
 
 /* ---- errors and status -------------------------------------------------- */
 
