@@ -107,6 +107,10 @@ _SIGS = {
                                          _U32, ctypes.POINTER(Plan), _U32, _VP]),
     "w8a16_kv_append": (_INT, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _U32]
                         + [ctypes.POINTER(HeadsDesc)] * 4 + [ctypes.POINTER(RopeDesc), _VP]),
+    "w8a16_kv_attention": (_INT, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _U32,
+                                  ctypes.POINTER(HeadsDesc), ctypes.POINTER(HeadsDesc), ctypes.c_float, _VP,
+                                  _U64, _VP]),
+    "w8a16_kv_attention_workspace_bytes": (_U64, [ctypes.POINTER(KvCacheDesc), _U32, _U32, _U32]),
     "w8a16_last_error": (ctypes.c_char_p, []),
     "w8a16_strerror": (ctypes.c_char_p, [_INT]),
     "w8a16_device_status": (_INT, [_VP, _INT, ctypes.POINTER(_U32), ctypes.POINTER(_U32),
@@ -677,6 +681,45 @@ def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_ou
     _check(_device_call(cache._index, stream, load().w8a16_kv_append, cache._ref, ctypes.byref(batch), act,
                         ctypes.byref(kd), ctypes.byref(vd), qd_ref, od_ref, ctypes.byref(rope)))
     return q_out
+
+
+def kv_attention_workspace_bytes(cache, batch, max_q, heads) -> int:
+    """Workspace bytes of kv_attention for `batch` sequences of up to `max_q` rows and
+    `heads` query heads, on the cache's device."""
+    import torch
+    with torch.cuda.device(cache._index):
+        n = int(load().w8a16_kv_attention_workspace_bytes(cache._ref, batch, max_q, heads))
+    if n == 0:
+        raise W8A16Error(-13, last_error())
+    return n
+
+
+def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu_q=None, max_q=None,
+                 workspace=None, stream=None):
+    """w8a16_kv_attention: causal attention of q [tokens, heads, head_dim] (bf16 or fp16,
+    already rotated) over the sequences' cached keys and values, the call's own tokens
+    (kv_append) included. page_table, lens, cu_q, max_q as in kv_append; softmax_scale
+    defaults to head_dim ** -0.5. workspace: a CUDA uint8 tensor of
+    kv_attention_workspace_bytes(...) bytes that no concurrent call uses (None allocates
+    one for this call). Returns out, [tokens, heads, head_dim] of q's dtype."""
+    import torch
+    rows = q.shape[0]
+    act = _act_type(q, "q")
+    batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    qd, od = _heads(cache, q, "q", rows, q.dtype), _heads(cache, out, "out", rows, q.dtype)
+    if workspace is None:
+        workspace = torch.empty(kv_attention_workspace_bytes(cache, batch.batch, batch.max_q, qd.heads),
+                                dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _same_gpu(cache._index, q, out, workspace)
+    if softmax_scale is None:
+        softmax_scale = cache.head_dim ** -0.5
+    _check(_device_call(cache._index, stream, load().w8a16_kv_attention, cache._ref, ctypes.byref(batch), act,
+                        ctypes.byref(qd), ctypes.byref(od), softmax_scale, workspace.data_ptr(), workspace.numel()))
+    return out
 
 
 def device_status(stream=None, clear=False) -> tuple[int, int, int]:

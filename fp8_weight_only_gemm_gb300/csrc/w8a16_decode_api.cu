@@ -129,4 +129,52 @@ int w8a16_kv_append(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* batch
     });
 }
 
+uint64_t w8a16_kv_attention_workspace_bytes(const w8a16_kv_cache_t* cache, uint32_t batch, uint32_t max_q, uint32_t heads) {
+    uint64_t bytes = 0;
+    guarded([&] {
+        const char* who = "w8a16_kv_attention_workspace_bytes";
+        int rc = check_cache(who, cache);
+        if (!rc && (batch < 1 || max_q < 1 || heads < 1 || heads % cache->kv_heads))
+            rc = api_fail(W8A16_ERR_ARG, std::string(who) + ": batch, max_q and heads must be positive, heads=" + u(heads) +
+                                             " a multiple of kv_heads=" + u(cache->kv_heads));
+        int sms = 0;
+        if (!rc) rc = w8a16::api_device(&sms);
+        if (rc) return rc;
+        bytes = w8a16::kv_attn_ws_bytes(cache->head_dim, sms);
+        return api_ok();
+    });
+    return bytes;
+}
+
+int w8a16_kv_attention(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* batch, uint32_t act_dtype,
+                       const w8a16_heads_t* q, const w8a16_heads_t* out, float softmax_scale, void* workspace,
+                       uint64_t workspace_bytes, w8a16_stream_t stream) {
+    return guarded([&] {
+        const char* who = "w8a16_kv_attention";
+        int rc = check_cache(who, cache);
+        if (!rc) rc = check_batch(who, cache, batch);
+        if (!rc) rc = check_act(who, act_dtype);
+        if (!rc) rc = check_heads(who, "q", q, 0);
+        if (!rc) rc = check_heads(who, "out", out, q->heads);
+        if (rc) return rc;
+        if (q->heads % cache->kv_heads)
+            return api_fail(W8A16_ERR_ARG, std::string(who) + ": " + u(q->heads) + " query heads do not divide among " +
+                                               u(cache->kv_heads) + " key/value heads");
+        if (!(softmax_scale > 0.f) || softmax_scale > 1e30f)
+            return api_fail(W8A16_ERR_ARG, std::string(who) + ": softmax_scale must be positive and finite");
+        int sms = 0;
+        rc = w8a16::api_device(&sms);
+        if (rc) return rc;
+        const uint64_t need = w8a16::kv_attn_ws_bytes(cache->head_dim, sms);
+        if (!workspace || workspace_bytes < need)
+            return api_fail(W8A16_ERR_ARG, std::string(who) + ": needs a workspace of " + u(need) + " bytes, got " +
+                                               u(workspace ? workspace_bytes : 0));
+        if (misaligned(workspace, 16)) return api_fail(W8A16_ERR_ALIGN, std::string(who) + ": the workspace must be 16-byte aligned");
+        std::string err;
+        rc = w8a16::launch_kv_attn(*cache, *batch, act_dtype, *q, *out, softmax_scale, workspace, sms,
+                                   reinterpret_cast<cudaStream_t>(stream), &err);
+        return rc ? api_fail(rc, err) : api_ok();
+    });
+}
+
 }  // extern "C"

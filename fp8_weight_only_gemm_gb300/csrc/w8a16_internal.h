@@ -281,6 +281,10 @@ cudaError_t gemv_status_read(StatusWord* out, bool clear, cudaStream_t s);
 int launch_kv_append(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& k,
                      const w8a16_heads_t& v, const w8a16_heads_t& q, const w8a16_heads_t& q_out,
                      const w8a16_rope_t& rope, cudaStream_t s, std::string* err);
+uint64_t kv_attn_ws_bytes(uint32_t head_dim, int sms);
+int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& q,
+                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms, cudaStream_t s, std::string* err);
+cudaError_t kv_attn_status_read(StatusWord* out, bool clear, cudaStream_t s);
 cudaError_t kv_append_status_read(StatusWord* out, bool clear, cudaStream_t s);
 
 // Shared by the C entries of every translation unit (w8a16_api.cu): the last error's

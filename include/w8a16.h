@@ -410,6 +410,36 @@ W8A16_API int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_batc
                               const w8a16_heads_t *q, const w8a16_heads_t *q_out,
                               const w8a16_rope_t *rope, w8a16_stream_t stream);
 
+/* w8a16_kv_attention -- attention of the call's queries over the cache:
+ *   out[n][hq] = sum_j softmax_j(softmax_scale * q[n][hq] . K[j][h]) V[j][h],  h = hq / (heads / kv_heads)
+ * over the positions j <= the query's own (causal from the end of the sequence; the
+ * cache already holds the call's tokens: w8a16_kv_append first).
+ *   q, out  [tokens][heads][head_dim], heads a multiple of kv_heads, BF16 or FP16
+ *           (act_dtype), same shape; out must not overlap q
+ * Scales may be any positive FP32 values (those below 2^-60 count as 2^-60). Both
+ * products take FP16 operands with FP32 sums: the E4M3 codes are exact, a query is
+ * exact down to 2^-21 of its head's largest element, and the softmax weights are
+ * rounded once to 11 bits. Queries without a visible key (lens[b] = 0, padding) give
+ * zeros; a query with a non-finite element gives NaN; what lies in slots past a
+ * query's position has no effect, whatever its bits.
+ *   workspace  device memory, 16-byte aligned, at least
+ *              w8a16_kv_attention_workspace_bytes(cache, batch->batch, batch->max_q,
+ *              heads) bytes; needs no clearing; calls that share one must be ordered
+ *              on one stream
+ * Two launches, queued as programmatic dependents that wait for the previous kernel
+ * before they touch memory. The grid depends on no length, so a captured call serves
+ * growing sequences. Deterministic. Sequences whose lens, cu_q or page numbers are out
+ * of range are reported (W8A16_STATUS_BAD_INDEX) and their outputs undefined. */
+W8A16_API int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_batch_t *batch,
+                                 uint32_t act_dtype, const w8a16_heads_t *q, const w8a16_heads_t *out,
+                                 float softmax_scale, void *workspace, uint64_t workspace_bytes,
+                                 w8a16_stream_t stream);
+
+/* Workspace bytes of w8a16_kv_attention on the current device (0, with a message, where
+ * there is none or the cache is invalid). */
+W8A16_API uint64_t w8a16_kv_attention_workspace_bytes(const w8a16_kv_cache_t *cache, uint32_t batch,
+                                                      uint32_t max_q, uint32_t heads);
+
 /* ---- errors and status -------------------------------------------------- */
 
 /* Message of the last failed call on this host thread ("" if none). */
