@@ -13,7 +13,7 @@ from .binding import (FLAG_PDL, Plan, VARIANT_AUTO, VARIANT_SIMT, VARIANT_TC, VA
                       split_activations, workspace_bytes, workspace_bytes_for, VARIANT_GEMV, VARIANT_STREAM,
                       header_functions, last_error, load, plan_current, plan_for, plan_variant, plan_ws,
                       quantize_weights, quantize_weights_ptr, selftest_wait_timeout, strerror,
-                      version, KVCache, kv_append, kv_attention, kv_attention_workspace_bytes)
+                      version, KVCache, kv_append, kv_attention, kv_attention_workspace_bytes, gemm_w4)
 
 __all__ = ["FLAG_PDL", "Plan", "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_TC", "VARIANT_TC8", "VARIANT_W8A8",
            "VARIANT_PRESPLIT", "WEIGHTS_BF16", "WEIGHTS_F32", "W8A16Error",
@@ -23,4 +23,4 @@ __all__ = ["FLAG_PDL", "Plan", "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_TC", "VA
            "header_functions", "last_error", "load", "plan_current", "plan_for", "plan_variant", "plan_ws",
            "quantize_weights", "quantize_weights_ptr", "selftest_wait_timeout", "strerror",
            "version", "KVCache", "kv_append", "kv_attention",
-           "kv_attention_workspace_bytes"]
+           "kv_attention_workspace_bytes", "gemm_w4"]

@@ -111,6 +111,7 @@ _SIGS = {
                                   ctypes.POINTER(HeadsDesc), ctypes.POINTER(HeadsDesc), ctypes.c_float, _VP,
                                   _U64, _VP]),
     "w8a16_kv_attention_workspace_bytes": (_U64, [ctypes.POINTER(KvCacheDesc), _U32, _U32, _U32]),
+    "w8a16_gemm_w4": (_INT, [_VP, _U32, _U32, _VP, _VP, _U32, _VP, _U32, _VP, _U32, _U32, _U32, _U32, _U32, _VP]),
     "w8a16_last_error": (ctypes.c_char_p, []),
     "w8a16_strerror": (ctypes.c_char_p, [_INT]),
     "w8a16_device_status": (_INT, [_VP, _INT, ctypes.POINTER(_U32), ctypes.POINTER(_U32),
@@ -720,6 +721,42 @@ def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu
     _check(_device_call(cache._index, stream, load().w8a16_kv_attention, cache._ref, ctypes.byref(batch), act,
                         ctypes.byref(qd), ctypes.byref(od), softmax_scale, workspace.data_ptr(), workspace.numel()))
     return out
+
+
+# ------------------------------------------------------------ 4-bit weights --
+def gemm_w4(A, W, scale, C=None, *, zeros=None, stream=None, flags: int = 0):
+    """w8a16_gemm_w4: C[:, :N] = A @ ((codes - zeros) * scale)^T for a few tokens.
+    A: bf16 or fp16 [M, K] (any row pitch that is a multiple of 8); W: uint8 [N, K/2], code
+    2j in the low half of byte j and 2j + 1 in its high half; scale: float32 or A's
+    dtype, [N, K/group] with group 32, 64 or 128 (taken from its shape); zeros: uint8
+    [N, K/group], 0..15 (None: 8); C: optional [M, >=N] of A's dtype."""
+    import torch
+    act = _act_type(A, "A")
+    if A.dim() != 2 or A.stride(1) != 1:
+        raise ValueError("A must be [M, K] with contiguous rows")
+    M, K = A.shape
+    if W.dim() != 2 or W.dtype is not torch.uint8 or not W.is_contiguous() or W.shape[1] * 2 != K:
+        raise ValueError(f"W must be contiguous uint8 [N, {K // 2}] (two codes a byte)")
+    N = W.shape[0]
+    if scale.dim() != 2 or scale.shape[0] != N or not scale.is_contiguous() or scale.shape[1] < 1 or K % scale.shape[1]:
+        raise ValueError(f"scale must be contiguous [{N}, K/group]; got {list(scale.shape)} for K={K}")
+    if scale.dtype is not torch.float32 and scale.dtype is not A.dtype:
+        raise TypeError(f"scale must be float32 or {A.dtype}, got {scale.dtype}")
+    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != scale.shape or not zeros.is_contiguous()):
+        raise ValueError(f"zeros must be contiguous uint8 {list(scale.shape)}")
+    if C is None:
+        C = torch.empty((M, N), dtype=A.dtype, device=A.device)
+    elif C.dtype is not A.dtype or C.dim() != 2 or C.stride(1) != 1 or C.shape[0] != M or C.shape[1] < N:
+        raise ValueError(f"C must be {A.dtype} [{M}, >={N}] with contiguous rows")
+    index = A.get_device()
+    if index < 0:
+        raise ValueError("all tensors must be on a CUDA device")
+    _same_gpu(index, W, scale, zeros, C)
+    _check(_device_call(index, stream, load().w8a16_gemm_w4, A.data_ptr(), A.stride(0), act, W.data_ptr(),
+                        scale.data_ptr(), 0 if scale.dtype is torch.float32 else 1,
+                        None if zeros is None else zeros.data_ptr(), K // scale.shape[1], C.data_ptr(), C.stride(0),
+                        M, N, K, flags))
+    return C
 
 
 def device_status(stream=None, clear=False) -> tuple[int, int, int]:

@@ -27,6 +27,16 @@ __device__ __forceinline__ uint32_t dsmem_map(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
+__device__ __forceinline__ void cluster_sync_all() {
+    cluster_arrive_release();
+    cluster_wait();
+}
+// The FP32 at this CTA's shared address `local`, in the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t local, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(dsmem_map(local, rank)) : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_async_v4f32(uint32_t remote_addr, uint32_t remote_bar, float a,
                                                float b, float c, float d) {
     asm volatile(

@@ -1,5 +1,5 @@
 // C entries of the decode-step operators around the GEMM: the paged 8-bit cache's
-// append and attention. All checks run on the host before any device work;
+// append and attention, and the product with 4-bit weights. All checks run on the host before any device work;
 // what only device memory tells (lengths, page numbers) the kernels check.
 #include <cuda_runtime.h>
 
@@ -173,6 +173,43 @@ int w8a16_kv_attention(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* ba
         std::string err;
         rc = w8a16::launch_kv_attn(*cache, *batch, act_dtype, *q, *out, softmax_scale, workspace, sms,
                                    reinterpret_cast<cudaStream_t>(stream), &err);
+        return rc ? api_fail(rc, err) : api_ok();
+    });
+}
+
+int w8a16_gemm_w4(const void* A, uint32_t a_row_stride, uint32_t act_dtype, const void* W, const void* scale,
+                  uint32_t scale_dtype, const void* zeros, uint32_t group, void* C, uint32_t c_row_stride, uint32_t M,
+                  uint32_t N, uint32_t K, uint32_t flags, w8a16_stream_t stream) {
+    return guarded([&] {
+        const std::string who("w8a16_gemm_w4");
+        if (flags & ~static_cast<uint32_t>(W8A16_FLAG_PDL)) return api_fail(W8A16_ERR_ARG, who + ": unknown flag bits " + u(flags));
+        if (M < 1) return api_fail(W8A16_ERR_M_ZERO, who + ": m=0 has no rows to compute");
+        if (group != 32 && group != 64 && group != 128)
+            return api_fail(W8A16_ERR_ARG, who + ": group=" + u(group) + " must be 32, 64 or 128");
+        if (K < group || K % group)
+            return api_fail(W8A16_ERR_K_BLOCK, who + ": K=" + u(K) + " must be a positive multiple of group=" + u(group));
+        if (a_row_stride < K || c_row_stride < N)
+            return api_fail(W8A16_ERR_PITCH, who + ": row pitches (a=" + u(a_row_stride) + ", c=" + u(c_row_stride) +
+                                                 ") must cover k=" + u(K) + " and n=" + u(N));
+        if (a_row_stride % 8)
+            return api_fail(W8A16_ERR_A_PITCH_ALIGN, who + ": a_row_stride=" + u(a_row_stride) + " must be a multiple of 8");
+        if (N < 1) return api_fail(W8A16_ERR_N_ZERO, who + ": n=0 has no columns to compute");
+        if (M > 65535u * 32u || N > 0x7FFFFFFFu / 8 || K > 0x7FFFFFFFu)
+            return api_fail(W8A16_ERR_RANGE, who + ": M=" + u(M) + ", N=" + u(N) + " or K=" + u(K) + " is out of range");
+        int rc = check_act(who.c_str(), act_dtype);
+        if (rc) return rc;
+        if (scale_dtype != W8A16_W4_SCALE_F32 && scale_dtype != W8A16_W4_SCALE_ACT)
+            return api_fail(W8A16_ERR_ARG, who + ": unknown scale type " + u(scale_dtype));
+        if (!A || !W || !scale || !C) return api_fail(W8A16_ERR_NULL, who + ": NULL operand pointer");
+        if (misaligned(A, 16) || misaligned(W, 16) || misaligned(scale, 4) || misaligned(zeros, 4) || misaligned(C, 2))
+            return api_fail(W8A16_ERR_ALIGN, who + ": alignment (A and W need 16 bytes, scale and zeros 4, C 2)");
+        int sms = 0;
+        rc = w8a16::api_device(&sms);
+        if (rc) return rc;
+        std::string err;
+        rc = w8a16::launch_w4({A, W, scale, zeros, C, a_row_stride, c_row_stride, M, N, K, group, act_dtype,
+                               scale_dtype == W8A16_W4_SCALE_F32},
+                              sms, flags, reinterpret_cast<cudaStream_t>(stream), &err);
         return rc ? api_fail(rc, err) : api_ok();
     });
 }

@@ -287,6 +287,15 @@ int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_
 cudaError_t kv_attn_status_read(StatusWord* out, bool clear, cudaStream_t s);
 cudaError_t kv_append_status_read(StatusWord* out, bool clear, cudaStream_t s);
 
+// ---- 4-bit weights (w8a16_w4.cu) ----
+struct W4Operands {
+    const void *A, *W, *scale, *zeros;
+    void* C;
+    uint32_t lda, ldc, M, N, K, group, act_dtype;
+    bool scale_f32;
+};
+int launch_w4(const W4Operands& o, int sms, uint32_t flags, cudaStream_t s, std::string* err);
+
 // Shared by the C entries of every translation unit (w8a16_api.cu): the last error's
 // message of this host thread, and the current device (sm_103 or an error).
 int api_fail(int code, const std::string& msg);

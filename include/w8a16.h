@@ -440,6 +440,35 @@ W8A16_API int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_b
 W8A16_API uint64_t w8a16_kv_attention_workspace_bytes(const w8a16_kv_cache_t *cache, uint32_t batch,
                                                       uint32_t max_q, uint32_t heads);
 
+/* ---- 4-bit weights ------------------------------------------------------- */
+
+/* Types of w8a16_gemm_w4's group scales. */
+enum {
+    W8A16_W4_SCALE_F32 = 0,
+    W8A16_W4_SCALE_ACT = 1   /* the activations' type */
+};
+
+/* w8a16_gemm_w4 -- the product with 4-bit weights and group scales, for a few tokens:
+ *   C[m][n] = sum_k A[m][k] * (code[n][k] - zero[n][k/group]) * scale[n][k/group]
+ *   A      BF16 or FP16 (act_dtype) [M][a_row_stride], 16-byte aligned, a_row_stride >= K
+ *          and a multiple of 8
+ *   W      [N][K/2] bytes, 16-byte aligned: byte j of a row holds code 2j in its low and
+ *          code 2j+1 in its high half
+ *   scale  [N][K/group], FP32 or the activations' type (scale_dtype), 4-byte aligned
+ *   zeros  [N][K/group] bytes in 0..15, 4-byte aligned, or NULL: 8 everywhere
+ *   group  32, 64 or 128; K a positive multiple of it
+ *   C      the activations' type [M][c_row_stride]; only columns < N are written
+ * code - zero is exact, the sums within a group are FP32 sums of exact products, and
+ * the scale multiplies each group's sum in FP32. One launch: a cluster of CTAs per
+ * 64 rows of W (128 above 8 tokens), tokens in tiles of up to 32 (each tile reads W
+ * again). Deterministic. flags: W8A16_FLAG_PDL (no work queued earlier on the stream may
+ * write W, scale or zeros); without it the call, queued as a programmatic dependent,
+ * waits for the previous kernel before it touches memory. Errors as w8a16_gemm. */
+W8A16_API int w8a16_gemm_w4(const void *A, uint32_t a_row_stride, uint32_t act_dtype, const void *W,
+                            const void *scale, uint32_t scale_dtype, const void *zeros, uint32_t group,
+                            void *C, uint32_t c_row_stride, uint32_t M, uint32_t N, uint32_t K,
+                            uint32_t flags, w8a16_stream_t stream);
+
 /* ---- errors and status -------------------------------------------------- */
 
 /* Message of the last failed call on this host thread ("" if none). */
