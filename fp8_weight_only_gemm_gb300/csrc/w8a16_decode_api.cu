@@ -83,6 +83,12 @@ int check_heads(const char* who, const char* name, const w8a16_heads_t* h, uint3
     return W8A16_OK;
 }
 
+// Query rows that share a key/value head, at most 2^31 - 1.
+uint32_t rows_per_head(uint32_t max_q, uint32_t heads, uint32_t kv_heads) {
+    const uint64_t r = static_cast<uint64_t>(max_q) * (heads / kv_heads);
+    return r > 0x7FFFFFFFu ? 0x7FFFFFFFu : static_cast<uint32_t>(r);
+}
+
 }  // namespace
 
 extern "C" {
@@ -140,7 +146,7 @@ uint64_t w8a16_kv_attention_workspace_bytes(const w8a16_kv_cache_t* cache, uint3
         int sms = 0;
         if (!rc) rc = w8a16::api_device(&sms);
         if (rc) return rc;
-        bytes = w8a16::kv_attn_ws_bytes(cache->head_dim, sms);
+        bytes = w8a16::kv_attn_ws_bytes(cache->head_dim, rows_per_head(max_q, heads, cache->kv_heads), sms);
         return api_ok();
     });
     return bytes;
@@ -165,13 +171,16 @@ int w8a16_kv_attention(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* ba
         int sms = 0;
         rc = w8a16::api_device(&sms);
         if (rc) return rc;
-        const uint64_t need = w8a16::kv_attn_ws_bytes(cache->head_dim, sms);
+        const uint64_t need = w8a16::kv_attn_ws_bytes(cache->head_dim, rows_per_head(batch->max_q, q->heads, cache->kv_heads), sms);
         if (!workspace || workspace_bytes < need)
             return api_fail(W8A16_ERR_ARG, std::string(who) + ": needs a workspace of " + u(need) + " bytes, got " +
                                                u(workspace ? workspace_bytes : 0));
         if (misaligned(workspace, 16)) return api_fail(W8A16_ERR_ALIGN, std::string(who) + ": the workspace must be 16-byte aligned");
         std::string err;
-        rc = w8a16::launch_kv_attn(*cache, *batch, act_dtype, *q, *out, softmax_scale, workspace, sms,
+        uint64_t timeout_ns = 0;
+        rc = w8a16::api_timeout(&timeout_ns);
+        if (rc) return rc;
+        rc = w8a16::launch_kv_attn(*cache, *batch, act_dtype, *q, *out, softmax_scale, workspace, sms, timeout_ns,
                                    reinterpret_cast<cudaStream_t>(stream), &err);
         return rc ? api_fail(rc, err) : api_ok();
     });

@@ -281,10 +281,12 @@ cudaError_t gemv_status_read(StatusWord* out, bool clear, cudaStream_t s);
 int launch_kv_append(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& k,
                      const w8a16_heads_t& v, const w8a16_heads_t& q, const w8a16_heads_t& q_out,
                      const w8a16_rope_t& rope, cudaStream_t s, std::string* err);
-uint64_t kv_attn_ws_bytes(uint32_t head_dim, int sms);
+uint64_t kv_attn_ws_bytes(uint32_t head_dim, uint32_t rows_per_head, int sms);
 int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& q,
-                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms, cudaStream_t s, std::string* err);
+                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms,
+                   uint64_t timeout_ns, cudaStream_t s, std::string* err);
 cudaError_t kv_attn_status_read(StatusWord* out, bool clear, cudaStream_t s);
+cudaError_t kv_attn_tc_status_read(StatusWord* out, bool clear, cudaStream_t s);
 cudaError_t kv_append_status_read(StatusWord* out, bool clear, cudaStream_t s);
 
 // ---- 4-bit weights (w8a16_w4.cu) ----
@@ -301,6 +303,7 @@ int launch_w4(const W4Operands& o, int sms, uint32_t flags, cudaStream_t s, std:
 int api_fail(int code, const std::string& msg);
 int api_ok();
 int api_device(int* sm_count);
+int api_timeout(uint64_t* ns);   // the limit of in-kernel waits (W8A16_WAIT_TIMEOUT_MS)
 
 // TMA descriptors of W ([N][K] E4M3, 128x128 boxes) and A ([M][K] BF16 at the
 // caller's pitch, 64 x token_tile boxes), 128-byte swizzle; cached per device.

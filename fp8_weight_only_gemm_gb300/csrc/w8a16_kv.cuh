@@ -19,10 +19,10 @@ struct Seq {
 __device__ __forceinline__ Seq sequence(const w8a16_kv_batch_t& bt, uint32_t page_size, uint32_t b) {
     int lo = static_cast<int>(b * bt.max_q), hi = lo + static_cast<int>(bt.max_q);
     if (bt.cu_q != nullptr) {
-        lo = __ldg(bt.cu_q + b);
-        hi = __ldg(bt.cu_q + b + 1);
+        lo = bt.cu_q[b];
+        hi = bt.cu_q[b + 1];
     }
-    const int len = __ldg(bt.lens + b);
+    const int len = bt.lens[b];
     const bool bad = lo < 0 || hi < lo || hi > static_cast<int>(bt.tokens) || hi - lo > static_cast<int>(bt.max_q) ||
                      len > static_cast<int>(bt.max_pages * page_size);
     return bad ? Seq{0, 0, 0, true} : Seq{lo, hi - lo, len, false};
@@ -34,7 +34,7 @@ __device__ __forceinline__ uint32_t seq_of_row(const w8a16_kv_batch_t& bt, uint3
     uint32_t lo = 0, hi = bt.batch;   // cu_q[lo] <= n < cu_q[hi]
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
-        if (__ldg(bt.cu_q + mid) <= static_cast<int>(n)) lo = mid;
+        if (bt.cu_q[mid] <= static_cast<int>(n)) lo = mid;
         else hi = mid;
     }
     return lo;

@@ -103,8 +103,8 @@ __device__ __forceinline__ void load_rotated(const uint16_t* head, const w8a16_r
     }
     if (!ch.rotated) return;
     const size_t row = static_cast<size_t>(pos) * (r.rotary_dim / 2) + 8 * i;
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(r.cos + row)), c1 = __ldg(reinterpret_cast<const float4*>(r.cos + row) + 1);
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(r.sin + row)), s1 = __ldg(reinterpret_cast<const float4*>(r.sin + row) + 1);
+    const float4 c0 = *reinterpret_cast<const float4*>(r.cos + row), c1 = reinterpret_cast<const float4*>(r.cos + row)[1];
+    const float4 s0 = *reinterpret_cast<const float4*>(r.sin + row), s1 = reinterpret_cast<const float4*>(r.sin + row)[1];
     const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
     const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
     if (r.interleaved) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
     const int page = begin / P + static_cast<int>(j);
     const int lo = max(begin, page * P), hi = min(seq.len, (page + 1) * P);   // this item's positions
     if (lo >= hi) return;
-    const int phys = __ldg(p.b.page_table + static_cast<int64_t>(b) * p.b.page_table_stride + page);
+    const int phys = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + page];
     if (phys < 0 || phys >= static_cast<int>(p.c.num_pages)) {
         if (lane == 0) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(phys));
         return;

@@ -32,7 +32,7 @@
 #include <cstring>
 #include <string>
 
-#include "w8a16_kv.cuh"
+#include "w8a16_kv_attn.cuh"
 
 namespace w8a16 {
 namespace {
@@ -44,7 +44,6 @@ constexpr uint32_t kRows = 16;                 // query rows of a tile (MMA M)
 constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (two n8 tiles; MMA K of the second product)
 constexpr uint32_t kUnitKeys = kWarps * kStepKeys;
 constexpr float kPBits = 15.f;                 // P is held times 2^15
-constexpr float kMinScale = 8.673617379884035e-19f;   // 2^-60
 
 template <uint32_t DP>
 struct Cfg {
@@ -57,17 +56,6 @@ struct Cfg {
     static constexpr uint32_t kStageBytes = 2 * kStepKeys * DP;
     static constexpr uint32_t kSmem = kWarps * kStages * kStageBytes;
     static_assert(kStages * kStageBytes >= kRows * DP * 4, "a warp's outputs fit its ring");
-};
-
-struct AttnArgs {
-    w8a16_kv_cache_t c;
-    w8a16_kv_batch_t b;
-    w8a16_heads_t q, out;
-    float* ws;
-    float scale_log2;       // softmax scale times log2(e)
-    uint32_t group;         // query heads per key/value head
-    uint32_t page_shift;
-    uint32_t ctas;          // of the attention kernel
 };
 
 // Workspace: slot (cta, which) = [kRows][DP] outputs, [kRows] maxima, [kRows] sums.
@@ -87,12 +75,6 @@ __device__ __forceinline__ uint64_t seq_units(const AttnArgs& p, uint32_t b, boo
     if (s.bad && report) record_failure(&g_kv_attn_status, W8A16_STATUS_BAD_INDEX, b);
     const Items it = items_of(p, s);
     return static_cast<uint64_t>(it.tiles) * it.units * p.c.kv_heads;
-}
-
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
 }
 
 // Units of the sequences before `b` and of all (every thread gets both).
@@ -153,23 +135,7 @@ __device__ __forceinline__ void find_unit(const AttnArgs& p, uint64_t at, uint64
     __syncthreads();
 }
 
-// The CTAs that get work (no more than there are units, so that none between the
-// first and the last CTA of an item is empty), the first unit of CTA c's range, and the
-// CTA that holds unit u.
-__device__ __forceinline__ uint64_t active_ctas(uint64_t units, uint32_t ctas) {
-    return units < ctas ? units : ctas;
-}
-__device__ __forceinline__ uint64_t first_unit(uint64_t c, uint64_t units, uint64_t ctas) { return c * units / ctas; }
-__device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t units, uint64_t ctas) {
-    return static_cast<uint32_t>(((u + 1) * ctas - 1) / units);
-}
-
 // ------------------------------------------------------------- primitives --
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -272,21 +238,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
             int bad = !finite;
             bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
             bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
-            // 2^(7 - E) in two factors: E reaches -133 for BF16 subnormals
-            const int E = mx > 0.f ? ilogbf(mx) : 7;
-            const int sh1 = (7 - E) / 2, sh2 = 7 - E - sh1;
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + sh1) << 23),
-                        f2 = __uint_as_float(static_cast<uint32_t>(127 + sh2) << 23);
-            const float g1 = __uint_as_float(static_cast<uint32_t>(127 - sh1) << 23),
-                        g2 = __uint_as_float(static_cast<uint32_t>(127 - sh2) << 23);
-            row_scale[r] = bad ? __uint_as_float(0x7FC00000u) : p.scale_log2 * g1 * g2;
+            const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
+            row_scale[r] = rs.scale;
 #pragma unroll
             for (uint32_t i = 0; i < C::kKChunks; ++i)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     float2 x = unpack2<F16>(raw[i][k]);
                     if (bad) x = make_float2(0.f, 0.f);   // the row's scale is NaN
-                    qf[i][k >> 1][(k & 1) * 2 + r] = pack2<true>(x.x * f1 * f2, x.y * f1 * f2);
+                    qf[i][k >> 1][(k & 1) * 2 + r] = pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
                 }
         }
         int tile_end, tile_min;   // keys any row, and every row, of the tile sees
@@ -306,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
             meta_k = 0.f;
             meta_v = 1.f;
             if (step + lane < nunits && key < tile_end) {
-                const int page = __ldg(p.b.page_table + static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift));
+                const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
                 if (page < 0 || page >= static_cast<int>(p.c.num_pages)) {
                     record_failure(&g_kv_attn_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(page));
                 } else {
@@ -635,14 +595,16 @@ uint32_t grid_ctas(uint32_t dp, int sms) { return static_cast<uint32_t>(sms) * (
 
 }  // namespace
 
-uint64_t kv_attn_ws_bytes(uint32_t head_dim, int sms) {
+uint64_t kv_attn_ws_bytes(uint32_t head_dim, uint32_t rows_per_head, int sms) {
+    if (kv_attn_tc_applies(head_dim, rows_per_head)) return kv_attn_tc_ws_bytes(head_dim, sms);
     const uint32_t dp = padded_dim(head_dim);
     return 8ull * grid_ctas(dp, sms) * slot_floats(dp);
 }
 
 int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& q,
-                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms, cudaStream_t s, std::string* err) {
-    AttnArgs p{c, b, q, out, static_cast<float*>(ws), softmax_scale * 1.4426950408889634f, q.heads / c.kv_heads, 0, 0};
+                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms,
+                   uint64_t timeout_ns, cudaStream_t s, std::string* err) {
+    AttnArgs p{c, b, q, out, static_cast<float*>(ws), softmax_scale * 1.4426950408889634f, q.heads / c.kv_heads, 0, 0, timeout_ns};
     while ((1u << p.page_shift) < c.page_size) ++p.page_shift;
     const uint32_t dp = padded_dim(c.head_dim);
     p.ctas = grid_ctas(dp, sms);
@@ -651,7 +613,8 @@ int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_
         return W8A16_ERR_RANGE;
     }
     const bool f16 = act_dtype == W8A16_ACT_F16;
-    const cudaError_t e = dp == 64    ? (f16 ? launch<true, 64>(p, s) : launch<false, 64>(p, s))
+    const cudaError_t e = kv_attn_tc_applies(c.head_dim, b.max_q * p.group) ? launch_kv_attn_tc(p, f16, sms, s)
+                          : dp == 64    ? (f16 ? launch<true, 64>(p, s) : launch<false, 64>(p, s))
                           : dp == 128 ? (f16 ? launch<true, 128>(p, s) : launch<false, 128>(p, s))
                                       : (f16 ? launch<true, 256>(p, s) : launch<false, 256>(p, s));
     if (e != cudaSuccess) {

@@ -1,0 +1,758 @@
+// Attention over the 8-bit paged cache for many query rows per key/value head (prompt
+// chunks): the mathematics of w8a16_kv_attn.cu on the 5th-generation tensor cores.
+//
+// Work. An item is 256 query rows (two tiles of 128; the G query heads of a key/value head
+// times the call's tokens) of one sequence and head, a unit 128 keys of it, with the
+// keys that no row of the item sees left out. The units of the whole call are split
+// over one CTA per SM in equal contiguous ranges; split items are joined through the
+// workspace by a second launch, in key order.
+//
+// A CTA. Warps 8-11 read a unit's E4M3 codes into registers a unit ahead, convert them to
+// FP16 (exact) and write the K and V tiles, [128 keys][DP] in 128-byte swizzled rows, two
+// stages each; the same layout serves K as a K-major operand and V, whose contraction
+// runs along its rows, as an MN-major one. Warps 0-3 and 4-7 own a row tile each; one
+// thread of each issues the tile's products, S = Q K^T (M = 128 rows, N = 128 keys) and
+// O += P V with P read from TMEM, so one tile's softmax runs under the other's products
+// (an issuing warp of its own would be a 13th, and leave 128 registers a thread instead of
+// 168). A thread owns a row, so no reduction crosses threads: a pass over the 128
+// scores in TMEM forms P in registers against the running maximum of the units before,
+// and only where a row's maximum has risen by more than 2^8 is the maximum moved, O
+// rescaled and the pass repeated (P <= 2^15 in FP16 either way). P overwrites S in TMEM.
+//
+// TMEM: S/P of the tiles at columns 0 and 128, O at 256 and 256 + DP.
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <string>
+
+#include "w8a16_cluster.cuh"
+#include "w8a16_kv_attn.cuh"
+
+namespace w8a16 {
+namespace {
+
+__device__ DeviceStatus g_kv_attn_tc_status;
+
+constexpr uint32_t kTile = 128;                // rows of a tile, and keys of a unit
+constexpr uint32_t kItemRows = 2 * kTile;
+constexpr uint32_t kSoftmaxWarps = 8, kConvWarps = 4;
+constexpr uint32_t kThreads = 32 * (kSoftmaxWarps + kConvWarps);
+constexpr uint32_t kWarpsAll = kThreads / 32;
+constexpr uint32_t kStages = 2;
+constexpr uint32_t kScaleRing = 4;             // units whose page scales are held (see the converters)
+constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
+constexpr uint32_t kChunk = 256;               // sequences whose unit counts are held at a time
+
+template <uint32_t DP>
+struct Cfg {
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;          // an FP16 tile
+    static constexpr uint32_t kHalfBytes = kTile * 128;             // a 64-column block of a tile
+    static constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
+    static constexpr uint32_t kTail = kV + kStages * kTileBytes;    // barriers, scales
+    static constexpr uint32_t kSmem = 1024 + kTail + 1024;
+};
+struct Tail {
+    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2], odone[2], drain[2];
+    uint32_t tmem;
+    int abort_flag;
+    int nan_seen;
+    float ks[kScaleRing][8], lv[kScaleRing][8], iv[kScaleRing][8];   // per 16 keys of a unit
+};
+static_assert(sizeof(Tail) <= 1024, "barrier block");
+
+enum Wait : unsigned { kWaitQ = 1, kWaitK, kWaitV, kWaitKFree, kWaitVFree, kWaitS, kWaitP, kWaitO, kWaitDrain };
+
+// ------------------------------------------------------------ the schedule --
+// Keys that the last row of row block rb sees, and the units of its item.
+__device__ __forceinline__ int block_end(const Seq& s, uint32_t group, uint32_t rb) {
+    const uint32_t rows = static_cast<uint32_t>(s.count) * group;
+    return s.len - s.count + static_cast<int>((min((rb + 1) * kItemRows, rows) - 1) / group) + 1;
+}
+__device__ __forceinline__ uint32_t block_units(const Seq& s, uint32_t group, uint32_t rb) {
+    return max(1, (block_end(s, group, rb) + static_cast<int>(kTile) - 1) / static_cast<int>(kTile));
+}
+__device__ __forceinline__ uint32_t seq_blocks(const Seq& s, uint32_t group) {
+    return s.len <= 0 ? 0u : (static_cast<uint32_t>(s.count) * group + kItemRows - 1) / kItemRows;
+}
+
+// Units per key/value head of up to kChunk sequences from b0, a warp per sequence.
+template <uint32_t WARPS>
+__device__ __forceinline__ uint32_t chunk_units(const AttnArgs& p, uint32_t b0, uint64_t* sh, bool report) {
+    const uint32_t count = min(kChunk, p.b.batch - b0);
+    for (uint32_t i = threadIdx.x >> 5; i < count; i += WARPS) {
+        const Seq s = sequence(p.b, p.c.page_size, b0 + i);
+        if (s.bad && report && (threadIdx.x & 31) == 0) record_failure(&g_kv_attn_tc_status, W8A16_STATUS_BAD_INDEX, b0 + i);
+        const uint32_t nb = seq_blocks(s, p.group);
+        uint64_t n = 0;
+        for (uint32_t rb = threadIdx.x & 31; rb < nb; rb += 32) n += block_units(s, p.group, rb);
+        n = warp_sum(n);
+        if ((threadIdx.x & 31) == 0) sh[i] = n;
+    }
+    __syncthreads();
+    return count;
+}
+
+// An item of the schedule: its sequence, head, row block, first unit (in the whole call's
+// order) and unit count.
+struct Item {
+    uint64_t first;
+    Seq s;
+    uint32_t b, h, rb, n;
+};
+__device__ __forceinline__ void next_item(const AttnArgs& p, Item& it) {
+    it.first += it.n;
+    if (++it.rb == seq_blocks(it.s, p.group)) {
+        it.rb = 0;
+        if (++it.h == p.c.kv_heads) {
+            it.h = 0;
+            do it.s = sequence(p.b, p.c.page_size, ++it.b);
+            while (seq_blocks(it.s, p.group) == 0);   // asked for only where units are left
+        }
+    }
+    it.n = block_units(it.s, p.group, it.rb);
+}
+template <uint32_t WARPS>
+__device__ uint64_t total_units(const AttnArgs& p, uint64_t* sh, bool report) {
+    uint64_t n = 0;
+    for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
+        const uint32_t count = chunk_units<WARPS>(p, b0, sh, report);
+        for (uint32_t i = 0; i < count; ++i) n += sh[i];
+        __syncthreads();
+    }
+    return n * p.c.kv_heads;
+}
+// The item that holds unit u (below the total).
+template <uint32_t WARPS>
+__device__ Item find_item(const AttnArgs& p, uint64_t u, uint64_t* sh) {
+    Item it{};
+    uint64_t base = 0;
+    for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
+        const uint32_t count = chunk_units<WARPS>(p, b0, sh, false);
+        for (uint32_t i = 0; i < count; ++i) {
+            const uint64_t n = sh[i] * p.c.kv_heads;
+            if (u < base + n) {
+                it.s = sequence(p.b, p.c.page_size, b0 + i);
+                it.b = b0 + i;
+                it.h = static_cast<uint32_t>((u - base) / sh[i]);
+                uint64_t rest = (u - base) % sh[i];
+                while (rest >= (it.n = block_units(it.s, p.group, it.rb))) {
+                    rest -= it.n;
+                    ++it.rb;
+                }
+                it.first = u - rest;
+                __syncthreads();
+                return it;
+            }
+            base += n;
+        }
+        __syncthreads();
+    }
+    return it;
+}
+
+// ------------------------------------------------------------- primitives --
+// FP16 operands, FP32 sums; B_MN: B is MN-major (its contraction runs along smem rows).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// MN-major operand of 128-byte swizzled rows: 8-row groups (along the contraction) 1024
+// bytes apart, 64-element column blocks kHalfBytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(block_bytes >> 4) << 16;     // leading byte offset: next 64 columns
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;            // stride byte offset: next 8 rows
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// A wait that gives up `timeout_ns` after it began, and tells the warp as one.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_tc_status, what);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
+    return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, timeout_ns, abort_flag, what));
+}
+
+// 16 codes -> 32 bytes of FP16.
+__device__ __forceinline__ void convert16(const uint4& q, uint4& lo, uint4& hi) {
+    e4m3x4_to_f16x4(q.x, lo.x, lo.y);
+    e4m3x4_to_f16x4(q.y, lo.z, lo.w);
+    e4m3x4_to_f16x4(q.z, hi.x, hi.y);
+    e4m3x4_to_f16x4(q.w, hi.z, hi.w);
+}
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& any) {
+    const uint32_t f = e4m3_nan_flags(w);
+    any |= f;
+    return w & ~((f >> 7) * 0xFFu);
+}
+
+// ----------------------------------------------------------------- kernel --
+template <bool F16, uint32_t DP>
+__global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs p) {
+    using C = Cfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t sh_units[kChunk];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Tail* const tl = reinterpret_cast<Tail*>(smem + C::kTail);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* const abort_flag = &tl->abort_flag;
+    const uint64_t tmo = p.timeout_ns;
+
+    if (warp == kSoftmaxWarps) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&tl->qfull[i]), 4);
+                mbar_init(smem_u32(&tl->kfull[i]), kConvWarps);
+                mbar_init(smem_u32(&tl->vfull[i]), kConvWarps);
+                mbar_init(smem_u32(&tl->kempty[i]), 2);   // both tiles' products
+                mbar_init(smem_u32(&tl->vempty[i]), 2);
+                mbar_init(smem_u32(&tl->sfull[i]), 2);   // the products' completion, and the issuer's own arrival
+                mbar_init(smem_u32(&tl->pfull[i]), 4);
+                mbar_init(smem_u32(&tl->odone[i]), 2);
+                mbar_init(smem_u32(&tl->drain[i]), 1);
+            }
+            tl->abort_flag = 0;
+            tl->nan_seen = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_u32(&tl->tmem), 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tl->tmem;
+
+    const uint64_t total = total_units<kWarpsAll>(p, sh_units, blockIdx.x == 0);
+    // sequences without keys: their rows are zero
+    for (uint32_t b = blockIdx.x; b < p.b.batch; b += gridDim.x) {
+        const Seq s = sequence(p.b, p.c.page_size, b);
+        if (s.bad || s.len > 0) continue;
+        const uint32_t per_row = p.out.heads * (p.c.head_dim / 8);
+        for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(s.count) * per_row; i += kThreads) {
+            const uint32_t n = static_cast<uint32_t>(i / per_row), h = static_cast<uint32_t>(i % per_row) / (p.c.head_dim / 8),
+                           d = static_cast<uint32_t>(i % (p.c.head_dim / 8)) * 8;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(s.first + static_cast<int>(n)) * p.out.token_stride +
+                                      static_cast<int64_t>(h) * p.out.head_stride + d) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const uint64_t ctas = active_ctas(total, p.ctas);
+    const bool works = blockIdx.x < ctas;
+    const uint64_t u0 = works ? first_unit(blockIdx.x, total, ctas) : 0, u_end = works ? first_unit(blockIdx.x + 1, total, ctas) : 0;
+    if (works) {
+        Item it = find_item<kWarpsAll>(p, u0, sh_units);
+        uint64_t u = u0;
+
+        if (warp < kSoftmaxWarps) {
+            // ------------------------------------------------------------ softmax
+            const uint32_t t = warp / 4, row = (warp % 4) * 32 + lane;      // row of the tile
+            const uint32_t lanes = ((warp % 4) * 32) << 16;
+            const uint32_t tS = tm + t * kTile + lanes, tO = tm + 2 * kTile + t * DP + lanes;
+            const bool issuer = warp % 4 == 0 && lane == 0;
+            constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
+            uint32_t blocks = 0, items = 0;   // units and items of this tile
+            bool first_part = true, ok = true;
+            // (issuer) S of the CTA's unit i, once its K tile is there
+            const auto scores = [&](uint32_t i) {
+                const uint32_t st = i % kStages;
+                if (!wait_one(smem_u32(&tl->kfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitK)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = (k / 4) * C::kHalfBytes + (k % 4) * 32;
+                    mma_ss(tm + t * kTile, smem_desc_kmajor_sw128(sbase + C::kQ + t * C::kTileBytes + off),
+                           smem_desc_kmajor_sw128(sbase + C::kK + st * C::kTileBytes + off), idS, k > 0);
+                }
+                tc_commit(smem_u32(&tl->sfull[t]));
+                mbar_arrive(smem_u32(&tl->sfull[t]));
+                tc_commit(smem_u32(&tl->kempty[st]));
+                return true;
+            };
+            // (issuer) O += P V of unit i, once P is written and its V tile is there
+            const auto outputs = [&](uint32_t i, uint32_t block, bool add) {
+                const uint32_t st = i % kStages;
+                if (!wait_one(smem_u32(&tl->pfull[t]), block & 1, tmo, abort_flag, kWaitP) ||
+                    !wait_one(smem_u32(&tl->vfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitV))
+                    return false;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t k = 0; k < kTile / 16; ++k)
+                    tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + 8 * k,
+                                  smem_desc_mn_sw128(sbase + C::kV + st * C::kTileBytes + k * 2048, C::kHalfBytes), idO, add || k > 0);
+                tc_commit(smem_u32(&tl->vempty[st]));
+                return true;
+            };
+            while (ok && u < u_end) {
+                const uint32_t j0 = static_cast<uint32_t>(u - it.first);
+                const uint32_t cnt = static_cast<uint32_t>(min(static_cast<uint64_t>(it.n - j0), u_end - u));
+                const uint32_t R = static_cast<uint32_t>(it.s.count) * p.group;
+                const uint32_t tile_row0 = it.rb * kItemRows + t * kTile;
+                if (tile_row0 < R) {
+                    // the query row, FP16, times 2^(7 - exponent of its maximum), 128-byte swizzled
+                    const uint32_t r = tile_row0 + row;
+                    const bool real = r < R;
+                    const uint32_t tok = real ? r / p.group : 0, head = it.h * p.group + (real ? r % p.group : 0);
+                    const int row_end = real ? it.s.len - it.s.count + static_cast<int>(tok) + 1 : 0x7FFFFFFF;
+                    const uint32_t r_w = min(tile_row0 + (warp % 4) * 32, R - 1);
+                    const int warp_min = it.s.len - it.s.count + static_cast<int>(r_w / p.group) + 1;
+                    const uint16_t* src = static_cast<const uint16_t*>(p.q.ptr) +
+                                          static_cast<int64_t>(it.s.first + static_cast<int>(tok)) * p.q.token_stride +
+                                          static_cast<int64_t>(head) * p.q.head_stride;
+                    float rowf;
+                    {
+                        float mx = 0.f;
+                        bool bad = false;
+#pragma unroll 4
+                        for (uint32_t d = 0; d < DP; d += 8) {
+                            uint4 a = make_uint4(0, 0, 0, 0);
+                            if (real && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
+                            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 x = unpack2<F16>(w[e]);
+                                bad = bad || !(fabsf(x.x) <= 3.4028235e38f) || !(fabsf(x.y) <= 3.4028235e38f);
+                                mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
+                            }
+                        }
+                        const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
+                        rowf = rs.scale;
+#pragma unroll 4
+                        for (uint32_t d = 0; d < DP; d += 8) {
+                            uint4 a = make_uint4(0, 0, 0, 0);
+                            if (real && !bad && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
+                            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 x = unpack2<F16>(w[e]);
+                                o[e] = pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
+                            }
+                            const uint32_t un = d / 8;
+                            *reinterpret_cast<uint4*>(smem + C::kQ + t * C::kTileBytes + (un / 8) * C::kHalfBytes + row * 128 +
+                                                      (((un % 8) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();   // the previous item's reads of O come before this one's products
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&tl->qfull[t]));
+                    const uint32_t unit0 = static_cast<uint32_t>(u - u0);   // the CTA's units, those of both tiles
+                    bool sent = true;
+                    if (issuer) sent = wait_one(smem_u32(&tl->qfull[t]), items & 1, tmo, abort_flag, kWaitQ) && scores(unit0);
+                    ok = __all_sync(0xFFFFFFFFu, sent);
+
+                    float ref = -INFINITY, l = 0.f;
+                    for (uint32_t j = 0; j < cnt && ok; ++j, ++blocks) {
+                        if (!(ok = wait_warp(smem_u32(&tl->sfull[t]), blocks & 1, tmo, abort_flag, kWaitS))) break;
+                        tc_fence_after();
+                        const uint32_t at = (unit0 + j) % kScaleRing;
+                        const int key0 = static_cast<int>((j0 + j) * kTile);
+                        const bool edge = key0 + static_cast<int>(kTile) > warp_min;
+                        uint32_t pk[64];
+                        float lsum;
+                        for (int pass = 0; pass < 2; ++pass) {
+                            const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
+                            float ymax = -INFINITY;
+                            lsum = 0.f;
+#pragma unroll
+                            for (uint32_t ch = 0; ch < 4; ++ch) {
+                                uint32_t v[32];
+                                tmem_ld32(tS + 32 * ch, v);
+                                tc_wait_ld();
+#pragma unroll
+                                for (uint32_t gq = 0; gq < 2; ++gq) {
+                                    const float f = tl->ks[at][2 * ch + gq] * rowf, lv = tl->lv[at][2 * ch + gq], iv = tl->iv[at][2 * ch + gq];
+                                    float s16 = 0.f;
+                                    if (!edge) {
+                                        float mx = __uint_as_float(v[16 * gq]);
+#pragma unroll
+                                        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(v[16 * gq + e]));
+                                        ymax = fmaxf(ymax, fmaf(mx, f, lv));
+                                        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(lv - rc, lv - rc);
+                                        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                                        for (int e = 0; e < 16; e += 2) {
+                                            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * gq + e]), __uint_as_float(v[16 * gq + e + 1])), ff, dd));
+                                            const float a = ex2(y.x), b = ex2(y.y);
+                                            s2.x += a;
+                                            s2.y += b;
+                                            pk[16 * ch + 8 * gq + e / 2] = pack2<true>(a, b);
+                                        }
+                                        s16 = s2.x + s2.y;
+                                    } else {
+#pragma unroll
+                                        for (int e = 0; e < 16; e += 2) {
+                                            float y0 = fmaf(__uint_as_float(v[16 * gq + e]), f, lv), y1 = fmaf(__uint_as_float(v[16 * gq + e + 1]), f, lv);
+                                            const int key = key0 + 32 * static_cast<int>(ch) + 16 * static_cast<int>(gq) + e;
+                                            if (key >= row_end) y0 = -INFINITY;
+                                            if (key + 1 >= row_end) y1 = -INFINITY;
+                                            ymax = fmaxf(ymax, fmaxf(y0, y1));
+                                            const float a = ex2(y0 - rc), b = ex2(y1 - rc);
+                                            s16 += a + b;
+                                            pk[16 * ch + 8 * gq + e / 2] = pack2<true>(a, b);
+                                        }
+                                    }
+                                    lsum = fmaf(s16, iv, lsum);
+                                }
+                            }
+                            if (!__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) break;
+                            // the maximum moves: earlier sums and outputs are rescaled, the unit is done again
+                            const float m_new = fmaxf(ref, ymax);
+                            const float a = ref == -INFINITY ? 0.f : ex2(ref - m_new);
+                            l *= a;
+                            ref = m_new;
+                            if (j > 0) {
+#pragma unroll 1
+                                for (uint32_t d = 0; d < DP; d += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + d, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                                    tmem_st_32x32b_x32(tO + d, o);
+                                }
+                                tc_wait_st();
+                            }
+                        }
+                        l += lsum;
+                        {
+                            uint32_t h0[32], h1[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                h0[e] = pk[e];
+                                h1[e] = pk[32 + e];
+                            }
+                            tmem_st_32x32b_x32(tS, h0);
+                            tmem_st_32x32b_x32(tS + 32, h1);
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&tl->pfull[t]));
+                        if (issuer) {
+                            sent = outputs(unit0 + j, blocks, j > 0);
+                            // S of the next unit overwrites P, which O's products, ahead of it in order, have then read
+                            if (sent && j + 1 < cnt) sent = scores(unit0 + j + 1);
+                            if (j + 1 == cnt) {
+                                tc_commit(smem_u32(&tl->odone[t]));
+                                mbar_arrive(smem_u32(&tl->odone[t]));
+                            }
+                        }
+                        ok = __all_sync(0xFFFFFFFFu, sent);
+                    }
+                    if (!ok || !(ok = wait_warp(smem_u32(&tl->odone[t]), items & 1, tmo, abort_flag, kWaitO))) break;
+                    ++items;
+                    tc_fence_after();
+                    // ---- outputs, or this range's part of them ([d][row], coalesced over rows)
+                    const bool whole = cnt == it.n;
+                    float* slot = p.ws + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * ((DP + 2) * kItemRows);
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(tok)) * p.out.token_stride +
+                                    static_cast<int64_t>(head) * p.out.head_stride;
+                    const bool poisoned = *static_cast<volatile int*>(&tl->nan_seen) != 0;
+#pragma unroll 1
+                    for (uint32_t d = 0; d < DP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + d, o);
+                        tc_wait_ld();
+                        if (poisoned && real) {
+                            // NaN values left out of the products at the causal edge: the rows that see them
+                            const int lo = max(static_cast<int>(j0 * kTile), (it.s.len - it.s.count + static_cast<int>(it.rb * kItemRows / p.group) + 1) / static_cast<int>(kTile) * static_cast<int>(kTile));
+                            const int hi = min(row_end, static_cast<int>((j0 + cnt) * kTile));
+                            for (int key = lo; key < hi; ++key) {
+                                const int page = p.b.page_table[static_cast<int64_t>(it.b) * p.b.page_table_stride + (key >> p.page_shift)];
+                                if (page < 0 || page >= static_cast<int>(p.c.num_pages)) continue;
+                                const uint8_t* vp = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(page) * p.c.page_stride +
+                                                    static_cast<int64_t>(it.h) * p.c.head_stride +
+                                                    static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (d + e < p.c.head_dim && (vp[d + e] & 0x7F) == 0x7F) o[e] = 0x7FC00000u;
+                            }
+                        }
+                        if (whole) {
+                            if (real) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8)
+                                    if (d + e < p.c.head_dim)
+                                        *reinterpret_cast<uint4*>(dst + d + e) =
+                                            make_uint4(pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
+                                                       pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
+                                                       pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
+                                                       pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) slot[(d + e) * kItemRows + t * kTile + row] = __uint_as_float(o[e]);
+                        }
+                    }
+                    if (!whole) {
+                        slot[DP * kItemRows + t * kTile + row] = ref;
+                        slot[(DP + 1) * kItemRows + t * kTile + row] = l;
+                    }
+                } else if (issuer) {
+                    // an item without this tile: its stages are released as they come
+                    for (uint32_t j = 0; j < cnt && ok; ++j) {
+                        const uint32_t i = static_cast<uint32_t>(u - u0) + j, st = i % kStages;
+                        ok = wait_one(smem_u32(&tl->kfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitK);
+                        if (ok) mbar_arrive(smem_u32(&tl->kempty[st]));
+                        ok = ok && wait_one(smem_u32(&tl->vfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitV);
+                        if (ok) mbar_arrive(smem_u32(&tl->vempty[st]));
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                first_part = false;
+                u += cnt;
+                if (u < u_end) next_item(p, it);
+            }
+            if (issuer) {   // every product issued ends before TMEM is released
+                tc_commit(smem_u32(&tl->drain[t]));
+                volatile int never = 0;
+                mbar_wait(smem_u32(&tl->drain[t]), 0, globaltimer_ns() + tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
+            }
+        } else {
+            // --------------------------------------------- codes -> FP16 tiles
+            constexpr uint32_t CH = DP / 16, kRowsPass = 128 / CH;   // 16-code chunks of a row; rows per pass
+            const uint32_t ct = threadIdx.x - 32 * kSoftmaxWarps, ch = ct % CH, r0 = ct / CH;
+            struct Unit {
+                int key0, end;
+                bool edge;
+                uint32_t b, h;
+            };
+            uint64_t un = u0;   // next unit to look up
+            const auto next_unit = [&](Unit& x) {
+                if (un >= u_end) return false;
+                if (un >= it.first + it.n) next_item(p, it);
+                x.key0 = static_cast<int>(un - it.first) * static_cast<int>(kTile);
+                x.end = block_end(it.s, p.group, it.rb);
+                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > it.s.len - it.s.count + static_cast<int>(it.rb * kItemRows / p.group) + 1;
+                x.b = it.b;
+                x.h = it.h;
+                ++un;
+                return true;
+            };
+            // lane l < 8: page and scales of keys [16 l, 16 l + 16) of a unit
+            int page = -1;
+            float mk = 0.f, mv = 1.f;
+            const auto load_meta = [&](const Unit& x) {
+                page = -1;
+                mk = 0.f;
+                mv = 1.f;
+                const int key = x.key0 + 16 * static_cast<int>(lane);
+                if (lane < 8 && key < x.end) {
+                    const int pg = p.b.page_table[static_cast<int64_t>(x.b) * p.b.page_table_stride + (key >> p.page_shift)];
+                    if (pg < 0 || pg >= static_cast<int>(p.c.num_pages)) {
+                        record_failure(&g_kv_attn_tc_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pg));
+                    } else {
+                        const int64_t s = static_cast<int64_t>(pg) * p.c.scale_page_stride + static_cast<int64_t>(x.h) * p.c.scale_head_stride;
+                        page = pg;
+                        mk = p.c.k_scale[s];
+                        mv = p.c.v_scale[s];
+                        if (mv < kMinScale) mv = kMinScale;
+                    }
+                }
+            };
+            const auto load_codes = [&](const Unit& x, const void* codes, uint4 (&q)[CH]) {
+#pragma unroll
+                for (uint32_t i = 0; i < CH; ++i) {
+                    const uint32_t r = i * kRowsPass + r0;
+                    const int key = x.key0 + static_cast<int>(r);
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r >> 4);
+                    q[i] = make_uint4(0, 0, 0, 0);
+                    if (pg >= 0 && key < x.end && 16 * ch < p.c.head_dim)
+                        q[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + static_cast<int64_t>(pg) * p.c.page_stride +
+                                                                    static_cast<int64_t>(x.h) * p.c.head_stride +
+                                                                    static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride +
+                                                                    16 * ch);
+                }
+            };
+            const auto store_tile = [&](uint32_t tile, const uint4 (&q)[CH], bool clean) {
+                uint32_t any = 0;
+#pragma unroll
+                for (uint32_t i = 0; i < CH; ++i) {
+                    const uint32_t r = i * kRowsPass + r0;
+                    uint4 c = q[i], lo, hi;
+                    if (clean) {
+                        c.x = drop_nan(c.x, any);
+                        c.y = drop_nan(c.y, any);
+                        c.z = drop_nan(c.z, any);
+                        c.w = drop_nan(c.w, any);
+                    }
+                    convert16(c, lo, hi);
+                    uint8_t* at = smem + tile + (ch / 4) * C::kHalfBytes + r * 128;
+                    const uint32_t un0 = (2 * ch) % 8;
+                    // the chunks of the second half store their halves in the other order: no bank is hit twice
+                    const bool swap = ch >= 4;
+                    *reinterpret_cast<uint4*>(at + (((un0 + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(at + (((un0 + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                }
+                if (any) *static_cast<volatile int*>(&tl->nan_seen) = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            Unit cur{}, ahead{};
+            uint4 kq[CH], vq[CH];
+            bool have = next_unit(cur);
+            load_meta(cur);
+            load_codes(cur, p.c.k_codes, kq);
+            load_codes(cur, p.c.v_codes, vq);
+            float sk = mk, sv = mv;
+            bool more = next_unit(ahead);
+            if (more) load_meta(ahead);
+            for (uint32_t i = 0; have; ++i) {
+                const uint32_t st = i % kStages, parity = ((i / kStages) & 1) ^ 1;
+                if (!wait_warp(smem_u32(&tl->kempty[st]), parity, tmo, abort_flag, kWaitKFree)) break;
+                store_tile(C::kK + st * C::kTileBytes, kq, false);
+                // Slot i % 4 is free: unit i - 4 was read before unit i - 2's products could free this K stage
+                if (warp == kSoftmaxWarps && lane < 8) {
+                    tl->ks[i % kScaleRing][lane] = sk;
+                    tl->lv[i % kScaleRing][lane] = __log2f(sv);
+                    tl->iv[i % kScaleRing][lane] = __frcp_rn(sv);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&tl->kfull[st]));
+                if (more) load_codes(ahead, p.c.k_codes, kq);
+                if (!wait_warp(smem_u32(&tl->vempty[st]), parity, tmo, abort_flag, kWaitVFree)) break;
+                store_tile(C::kV + st * C::kTileBytes, vq, cur.edge);
+                if (lane == 0) mbar_arrive(smem_u32(&tl->vfull[st]));
+                have = more;
+                if (more) {
+                    load_codes(ahead, p.c.v_codes, vq);
+                    cur = ahead;
+                    sk = mk;
+                    sv = mv;
+                    more = next_unit(ahead);
+                    if (more) load_meta(ahead);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftmaxWarps) tmem_dealloc(tm, 512);
+}
+
+// Joins the parts of split items in key order. blockIdx.x = c - 1 for the boundary before
+// CTA c's range, which does the item if it is the first boundary inside it;
+// blockIdx.y = 16 dims, a thread a row.
+constexpr uint32_t kJoinThreads = kItemRows, kJoinDims = 16;
+template <bool F16>
+__global__ void __launch_bounds__(kJoinThreads) kv_attn_tc_join_kernel(const AttnArgs p, uint32_t dp) {
+    __shared__ uint64_t sh_units[kChunk];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const uint64_t total = total_units<kJoinThreads / 32>(p, sh_units, false);
+    const uint64_t ctas = active_ctas(total, p.ctas);
+    const uint32_t c = blockIdx.x + 1, d0 = blockIdx.y * kJoinDims;
+    if (c >= ctas || d0 >= p.c.head_dim) return;
+    const uint64_t u = first_unit(c, total, ctas);
+    const Item it = find_item<kJoinThreads / 32>(p, u, sh_units);
+    if (it.first == u || first_unit(c - 1, total, ctas) > it.first) return;
+    const uint32_t c0 = c - 1, c1 = cta_of(it.first + it.n - 1, total, ctas);
+    const uint32_t row = threadIdx.x, r = it.rb * kItemRows + row;
+    if (r >= static_cast<uint32_t>(it.s.count) * p.group) return;
+    const uint64_t stride = static_cast<uint64_t>(dp + 2) * kItemRows;
+    const uint64_t slot0 = first_unit(c0, total, ctas) == it.first ? 2ull * c0 : 2ull * c0 + 1;   // c0's first part, or its last
+    const auto slot = [&](uint32_t cta) { return p.ws + (cta == c0 ? slot0 : 2ull * cta) * stride; };
+    float m = -INFINITY;
+    for (uint32_t i = c0; i <= c1; ++i) m = fmaxf(m, slot(i)[dp * kItemRows + row]);
+    float acc[kJoinDims] = {}, l = 0.f;
+    for (uint32_t i = c0; i <= c1; ++i) {
+        const float* s = slot(i);
+        const float mi = s[dp * kItemRows + row];
+        const float a = mi == -INFINITY ? 0.f : ex2(mi - m);
+        l = fmaf(a, s[(dp + 1) * kItemRows + row], l);
+#pragma unroll
+        for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] = fmaf(a, s[(d0 + d) * kItemRows + row], acc[d]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(r / p.group)) * p.out.token_stride +
+                    static_cast<int64_t>(it.h * p.group + r % p.group) * p.out.head_stride + d0;
+    uint32_t w[kJoinDims / 2];
+#pragma unroll
+    for (uint32_t d = 0; d < kJoinDims / 2; ++d) w[d] = pack2<F16>(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool F16, uint32_t DP>
+cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_tc_kernel<F16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(p.ctas, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv_attn_tc_kernel<F16, DP>, p);
+    if (e != cudaSuccess || p.ctas < 2) return e;
+    cfg.gridDim = dim3(p.ctas - 1, (p.c.head_dim + kJoinDims - 1) / kJoinDims, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv_attn_tc_join_kernel<F16>, p, DP);
+}
+
+}  // namespace
+
+// Heads above 128 leave no room in TMEM for two row tiles' outputs.
+bool kv_attn_tc_applies(uint32_t head_dim, uint32_t rows_per_head) { return head_dim <= 128 && rows_per_head >= 64; }
+
+uint64_t kv_attn_tc_ws_bytes(uint32_t head_dim, int sms) {
+    return 8ull * static_cast<uint32_t>(sms) * ((head_dim <= 64 ? 64u : 128u) + 2) * kItemRows;
+}
+
+cudaError_t launch_kv_attn_tc(AttnArgs p, bool f16, int sms, cudaStream_t s) {
+    p.ctas = static_cast<uint32_t>(sms);
+    if (p.c.head_dim <= 64) return f16 ? launch<true, 64>(p, s) : launch<false, 64>(p, s);
+    return f16 ? launch<true, 128>(p, s) : launch<false, 128>(p, s);
+}
+
+cudaError_t kv_attn_tc_status_read(StatusWord* out, bool clear, cudaStream_t s) {
+    DeviceStatus st;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&st, g_kv_attn_tc_status, sizeof st, 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+    out->code = st.code;
+    out->where = st.where;
+    out->detail = st.detail;
+    if (clear) {
+        const DeviceStatus zero{0, 0, 0};
+        e = cudaMemcpyToSymbolAsync(g_kv_attn_tc_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
+
+}  // namespace w8a16

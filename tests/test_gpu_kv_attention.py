@@ -248,3 +248,69 @@ def test_refusals(w8):
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         with pytest.raises(w8.W8A16Error):
             w8.kv_attention(c, q, t, n, softmax_scale=bad)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,dtype", [(128, 8, 1, "bf16"), (64, 4, 4, "f16"), (112, 6, 2, "bf16"), (16, 2, 1, "f16")])
+def test_many_rows_ragged(w8, D, Hq, Hkv, dtype):
+    """Row blocks that are full, ragged and single-tiled, items split between CTAs, padding
+    rows, sequences without rows or keys."""
+    case = Case([700, 1200, 300, 64, 0, 257], [130, 257, 300, 0, 3, 90], Hq, Hkv, D, 32, dtype, seed=D)
+    finite_cache(case, 30)
+    check(case, w8)
+
+
+def test_many_rows_long_context(w8):
+    case = Case([20011], [70], 4, 1, 128, 64, "bf16", seed=31)
+    finite_cache(case, 31)
+    check(case, w8, uniform=True)
+    case = Case([3001, 2999], [40, 40], 4, 2, 64, 16, "f16", seed=32)
+    finite_cache(case, 32, pow2=False)
+    check(case, w8, uniform=True, scale=0.5)
+
+
+def test_many_rows_sharp_softmax_and_wide_scales(w8):
+    case = Case([900, 500], [100, 100], 2, 2, 64, 16, "bf16", seed=33)
+    finite_cache(case, 33)
+    g = torch.Generator().manual_seed(1)
+    case.vs = torch.where(case.vs.isnan(), case.vs, 2.0 ** torch.randint(-30, 11, case.vs.shape, generator=g).float())
+    check(case, w8, uniform=True, q_scale=4.0)
+
+
+def test_many_rows_nan_reaches_only_the_rows_that_see_it(w8):
+    case = Case([300, 150], [150, 150], 2, 1, 64, 16, "bf16", seed=34)
+    finite_cache(case, 34)
+    for b, pos, d in ((0, 250, 10), (0, 20, 11), (1, 149, 12), (1, 0, 13)):
+        case.vc[int(case.table[b, pos // 16]), 0, pos % 16, d] = 0x7F
+    case.kc[int(case.table[0, 290 // 16]), 0, 290 % 16, 5] = 0xFF
+    case.qkv[7, 1, 2] = float("-inf")
+    case.to_gpu(w8)
+    out = w8.kv_attention(case.cache, case.q, case.dtable, case.dlens)
+    nan = out.isnan().cpu()
+    want = torch.zeros_like(nan)
+    want[100:150, :, 10] = True                  # row t of sequence 0 has position 150 + t
+    want[:150, :, 11] = True
+    want[140:150] = True
+    want[299, :, 12] = True
+    want[150:, :, 13] = True
+    want[7, 1] = True
+    assert torch.equal(nan, want)
+    assert w8.device_status(clear=True)[0] == 0
+
+
+def test_many_rows_repeatable_strides_and_graph(w8):
+    case = Case([1000, 600], [80, 80], 4, 2, 128, 16, "bf16", seed=35, slot_major=True, fused=True)
+    finite_cache(case, 35)
+    got = check(case, w8, uniform=True)
+    ws = torch.full((w8.kv_attention_workspace_bytes(case.cache, 2, 80, 4),), 0xFF, dtype=torch.uint8, device="cuda")
+    wide = torch.zeros(160, 4, 136, dtype=torch.bfloat16, device="cuda")
+    w8.kv_attention(case.cache, case.q, case.dtable, case.dlens, wide[:, :, :128], workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w8.kv_attention(case.cache, case.q, case.dtable, case.dlens, wide[:, :, :128], workspace=ws)
+    wide.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(wide[:, :, :128].double().cpu().numpy(), got) and wide[:, :, 128:].abs().sum() == 0
+    bad = w8.kv_attention(case.cache, case.q, case.dtable + 100000, case.dlens)
+    assert bad.shape == case.q.shape and w8.device_status(clear=True)[0] == 2
