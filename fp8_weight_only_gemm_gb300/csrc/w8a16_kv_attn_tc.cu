@@ -15,9 +15,10 @@
 // O += P V with P read from TMEM, so one tile's softmax runs under the other's products
 // (an issuing warp of its own would be a 13th, and leave 128 registers a thread instead of
 // 168). A thread owns a row, so no reduction crosses threads: a pass over the 128
-// scores in TMEM forms P in registers against the running maximum of the units before,
-// and only where a row's maximum has risen by more than 2^8 is the maximum moved, O
-// rescaled and the pass repeated (P <= 2^15 in FP16 either way). P overwrites S in TMEM.
+// scores in TMEM finds the unit's maximum, and only where it exceeds the running one by more
+// than 8 is that moved and O rescaled; a second pass writes P (at most 2^15, FP16) over the
+// columns of S that it has read. (One pass that forms P in registers against the old maximum
+// and is repeated where that fails was slower: its unrolled code missed the instruction cache.)
 //
 // TMEM: S/P of the tiles at columns 0 and 128, O at 256 and 256 + DP.
 #include <cuda_runtime.h>
@@ -207,6 +208,63 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& any) {
     return w & ~((f >> 7) * 0xFFu);
 }
 
+// 32 scores of a row (columns 32 ch of a unit): the largest y = score * ks * rowf +
+// log2(vs) of the keys before `end` (EDGE; else of all).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <bool EDGE>
+__device__ __forceinline__ float chunk_max(const uint32_t (&v)[32], const Tail* tl, uint32_t at, uint32_t ch, float rowf, int end) {
+    float y = -INFINITY;
+#pragma unroll
+    for (uint32_t g = 0; g < 2; ++g) {
+        const float f = tl->ks[at][2 * ch + g] * rowf, lv = tl->lv[at][2 * ch + g];
+        float mx = -INFINITY;   // f >= 0: the largest score gives the largest y
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            float a = __uint_as_float(v[16 * g + e]), b = __uint_as_float(v[16 * g + e + 1]);
+            if (EDGE) {
+                const int k = 32 * static_cast<int>(ch) + 16 * static_cast<int>(g) + e;
+                if (k >= end) a = -INFINITY;
+                if (k + 1 >= end) b = -INFINITY;
+            }
+            mx = max3(mx, a, b);
+        }
+        if (!EDGE || mx != -INFINITY) y = fmaxf(y, fmaf(mx, f, lv));
+    }
+    return y;
+}
+// Their weights 2^(y - rc) as FP16 pairs; returns the sum of weight / vs.
+template <bool EDGE>
+__device__ __forceinline__ float chunk_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, uint32_t ch, float rowf,
+                                               float rc, int end, uint32_t (&pk)[16]) {
+    float sum = 0.f;
+#pragma unroll
+    for (uint32_t g = 0; g < 2; ++g) {
+        const float f = tl->ks[at][2 * ch + g] * rowf, d = tl->lv[at][2 * ch + g] - rc;
+        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(d, d);
+        uint64_t s2 = pack_f32x2(0.f, 0.f);
+        const uint64_t one = pack_f32x2(1.f, 1.f);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1])), ff, dd));
+            if (EDGE) {
+                const int k = 32 * static_cast<int>(ch) + 16 * static_cast<int>(g) + e;
+                if (k >= end) y.x = -INFINITY;
+                if (k + 1 >= end) y.y = -INFINITY;
+            }
+            const float a = ex2(y.x), b = ex2(y.y);
+            s2 = fma_f32x2(pack_f32x2(a, b), one, s2);
+            pk[8 * g + e / 2] = pack2<true>(a, b);
+        }
+        const float2 s = unpack_f32x2(s2);
+        sum = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], sum);
+    }
+    return sum;
+}
+
 // ----------------------------------------------------------------- kernel --
 template <bool F16, uint32_t DP>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs p) {
@@ -373,83 +431,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         const uint32_t at = (unit0 + j) % kScaleRing;
                         const int key0 = static_cast<int>((j0 + j) * kTile);
                         const bool edge = key0 + static_cast<int>(kTile) > warp_min;
-                        uint32_t pk[64];
-                        float lsum;
-                        for (int pass = 0; pass < 2; ++pass) {
-                            const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
-                            float ymax = -INFINITY;
-                            lsum = 0.f;
+                        // ---- the unit's maximum, against which `ref` is good enough or moves
+                        float ymax = -INFINITY;
+                        uint32_t v[2][32];
+                        tmem_ld32(tS, v[0]);
+#pragma unroll 1
+                        for (uint32_t ch = 0; ch < 4; ch += 2)
 #pragma unroll
-                            for (uint32_t ch = 0; ch < 4; ++ch) {
-                                uint32_t v[32];
-                                tmem_ld32(tS + 32 * ch, v);
+                            for (uint32_t half = 0; half < 2; ++half) {
                                 tc_wait_ld();
-#pragma unroll
-                                for (uint32_t gq = 0; gq < 2; ++gq) {
-                                    const float f = tl->ks[at][2 * ch + gq] * rowf, lv = tl->lv[at][2 * ch + gq], iv = tl->iv[at][2 * ch + gq];
-                                    float s16 = 0.f;
-                                    if (!edge) {
-                                        float mx = __uint_as_float(v[16 * gq]);
-#pragma unroll
-                                        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(v[16 * gq + e]));
-                                        ymax = fmaxf(ymax, fmaf(mx, f, lv));
-                                        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(lv - rc, lv - rc);
-                                        float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-                                        for (int e = 0; e < 16; e += 2) {
-                                            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * gq + e]), __uint_as_float(v[16 * gq + e + 1])), ff, dd));
-                                            const float a = ex2(y.x), b = ex2(y.y);
-                                            s2.x += a;
-                                            s2.y += b;
-                                            pk[16 * ch + 8 * gq + e / 2] = pack2<true>(a, b);
-                                        }
-                                        s16 = s2.x + s2.y;
-                                    } else {
-#pragma unroll
-                                        for (int e = 0; e < 16; e += 2) {
-                                            float y0 = fmaf(__uint_as_float(v[16 * gq + e]), f, lv), y1 = fmaf(__uint_as_float(v[16 * gq + e + 1]), f, lv);
-                                            const int key = key0 + 32 * static_cast<int>(ch) + 16 * static_cast<int>(gq) + e;
-                                            if (key >= row_end) y0 = -INFINITY;
-                                            if (key + 1 >= row_end) y1 = -INFINITY;
-                                            ymax = fmaxf(ymax, fmaxf(y0, y1));
-                                            const float a = ex2(y0 - rc), b = ex2(y1 - rc);
-                                            s16 += a + b;
-                                            pk[16 * ch + 8 * gq + e / 2] = pack2<true>(a, b);
-                                        }
-                                    }
-                                    lsum = fmaf(s16, iv, lsum);
-                                }
+                                // (after the last chunk: the first again, for the pass below)
+                                tmem_ld32(tS + 32 * ((ch + half + 1) % 4), v[half ^ 1]);
+                                ymax = fmaxf(ymax, edge ? chunk_max<true>(v[half], tl, at, ch + half, rowf, row_end - key0)
+                                                        : chunk_max<false>(v[half], tl, at, ch + half, rowf, 0));
                             }
-                            if (!__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) break;
-                            // the maximum moves: earlier sums and outputs are rescaled, the unit is done again
+                        if (__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) {
                             const float m_new = fmaxf(ref, ymax);
                             const float a = ref == -INFINITY ? 0.f : ex2(ref - m_new);
                             l *= a;
                             ref = m_new;
                             if (j > 0) {
+                                tc_wait_ld();
 #pragma unroll 1
                                 for (uint32_t d = 0; d < DP; d += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(tO + d, o);
+                                    tmem_ld32(tO + d, v[1]);
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                                    tmem_st_32x32b_x32(tO + d, o);
+                                    for (int e = 0; e < 32; ++e) v[1][e] = __float_as_uint(__uint_as_float(v[1][e]) * a);
+                                    tmem_st_32x32b_x32(tO + d, v[1]);
                                 }
-                                tc_wait_st();
                             }
                         }
-                        l += lsum;
-                        {
-                            uint32_t h0[32], h1[32];
+                        // ---- P, over the columns of S that have been read
+                        const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
+#pragma unroll 1
+                        for (uint32_t ch = 0; ch < 4; ch += 2)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                h0[e] = pk[e];
-                                h1[e] = pk[32 + e];
+                            for (uint32_t half = 0; half < 2; ++half) {
+                                tc_wait_ld();
+                                if (ch + half < 3) tmem_ld32(tS + 32 * (ch + half + 1), v[half ^ 1]);
+                                uint32_t pk[16];
+                                l += edge ? chunk_weights<true>(v[half], tl, at, ch + half, rowf, rc, row_end - key0, pk)
+                                          : chunk_weights<false>(v[half], tl, at, ch + half, rowf, rc, 0, pk);
+                                tmem_st_32x32b_x16(tS + 16 * (ch + half), pk);
                             }
-                            tmem_st_32x32b_x32(tS, h0);
-                            tmem_st_32x32b_x32(tS + 32, h1);
-                        }
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
