@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
                     meta_page = page;
                     meta_k = p.c.k_scale[at];
                     meta_v = p.c.v_scale[at];
+                    if (meta_k < kMinScale) meta_k = kMinScale;
                     if (meta_v < kMinScale) meta_v = kMinScale;
                 }
             }

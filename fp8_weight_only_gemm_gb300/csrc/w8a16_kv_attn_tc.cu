@@ -14,11 +14,9 @@
 // thread of each issues the tile's products, S = Q K^T (M = 128 rows, N = 128 keys) and
 // O += P V with P read from TMEM, so one tile's softmax runs under the other's products
 // (an issuing warp of its own would be a 13th, and leave 128 registers a thread instead of
-// 168). A thread owns a row, so no reduction crosses threads: a pass over the 128
-// scores in TMEM finds the unit's maximum, and only where it exceeds the running one by more
-// than 8 is that moved and O rescaled; a second pass writes P (at most 2^15, FP16) over the
-// columns of S that it has read. (One pass that forms P in registers against the old maximum
-// and is repeated where that fails was slower: its unrolled code missed the instruction cache.)
+// 168). A thread owns a row, so no reduction crosses threads: it reads its
+// 128 scores from TMEM, and only where a unit's maximum exceeds the running one by more than
+// 8 is that moved and O rescaled; P (at most 2^15, FP16) overwrites the columns of S.
 //
 // TMEM: S/P of the tiles at columns 0 and 128, O at 256 and 256 + DP.
 #include <cuda_runtime.h>
@@ -69,6 +67,10 @@ __device__ __forceinline__ int block_end(const Seq& s, uint32_t group, uint32_t 
     const uint32_t rows = static_cast<uint32_t>(s.count) * group;
     return s.len - s.count + static_cast<int>((min((rb + 1) * kItemRows, rows) - 1) / group) + 1;
 }
+// Keys that its first row sees.
+__device__ __forceinline__ int edge_key(const Seq& s, uint32_t group, uint32_t rb) {
+    return s.len - s.count + static_cast<int>(rb * kItemRows / group) + 1;
+}
 __device__ __forceinline__ uint32_t block_units(const Seq& s, uint32_t group, uint32_t rb) {
     return max(1, (block_end(s, group, rb) + static_cast<int>(kTile) - 1) / static_cast<int>(kTile));
 }
@@ -113,7 +115,7 @@ __device__ __forceinline__ void next_item(const AttnArgs& p, Item& it) {
     it.n = block_units(it.s, p.group, it.rb);
 }
 template <uint32_t WARPS>
-__device__ uint64_t total_units(const AttnArgs& p, uint64_t* sh, bool report) {
+__device__ __noinline__ uint64_t total_units(const AttnArgs& p, uint64_t* sh, bool report) {
     uint64_t n = 0;
     for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
         const uint32_t count = chunk_units<WARPS>(p, b0, sh, report);
@@ -124,7 +126,7 @@ __device__ uint64_t total_units(const AttnArgs& p, uint64_t* sh, bool report) {
 }
 // The item that holds unit u (below the total).
 template <uint32_t WARPS>
-__device__ Item find_item(const AttnArgs& p, uint64_t u, uint64_t* sh) {
+__device__ __noinline__ Item find_item(const AttnArgs& p, uint64_t u, uint64_t* sh) {
     Item it{};
     uint64_t base = 0;
     for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
@@ -186,10 +188,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-// A wait that gives up `timeout_ns` after it began, and tells the warp as one.
+// 8 columns of a warp's lanes, times f.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8], float f) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(v[0] * f),
+                 "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f), "f"(v[6] * f), "f"(v[7] * f)
+                 : "memory");
+}
+
+// A wait that gives up `timeout_ns` after it began, and tells the warp as one. (What is
+// rarely run is kept out of line: the loops' code has to stay in the instruction cache.)
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
+    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_tc_status, what);
+}
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
     if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_tc_status, what);
+    return wait_slow(bar, parity, timeout_ns, abort_flag, what);
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
     return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, timeout_ns, abort_flag, what));
@@ -208,61 +221,67 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& any) {
     return w & ~((f >> 7) * 0xFFu);
 }
 
-// 32 scores of a row (columns 32 ch of a unit): the largest y = score * ks * rowf +
-// log2(vs) of the keys before `end` (EDGE; else of all).
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-template <bool EDGE>
-__device__ __forceinline__ float chunk_max(const uint32_t (&v)[32], const Tail* tl, uint32_t at, uint32_t ch, float rowf, int end) {
+
+// 32 scores of a row, columns `first` on: those of keys from `end` on are masked.
+__device__ __forceinline__ void mask_scores(uint32_t (&v)[32], int first, int end) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (first + e >= end) v[e] = 0xFF800000u;
+}
+// Their largest y = score ks rowf + log2(vs) (ks rowf > 0: the largest score gives the largest y).
+__device__ __forceinline__ float score_max(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf) {
     float y = -INFINITY;
 #pragma unroll
-    for (uint32_t g = 0; g < 2; ++g) {
-        const float f = tl->ks[at][2 * ch + g] * rowf, lv = tl->lv[at][2 * ch + g];
-        float mx = -INFINITY;   // f >= 0: the largest score gives the largest y
+    for (int g = 0; g < 2; ++g) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            float a = __uint_as_float(v[16 * g + e]), b = __uint_as_float(v[16 * g + e + 1]);
-            if (EDGE) {
-                const int k = 32 * static_cast<int>(ch) + 16 * static_cast<int>(g) + e;
-                if (k >= end) a = -INFINITY;
-                if (k + 1 >= end) b = -INFINITY;
-            }
-            mx = max3(mx, a, b);
-        }
-        if (!EDGE || mx != -INFINITY) y = fmaxf(y, fmaf(mx, f, lv));
+        for (int e = 0; e < 16; e += 2) mx = max3(mx, __uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1]));
+        y = fmaxf(y, fmaf(mx, tl->ks[at][2 * ch + g] * rowf, tl->lv[at][2 * ch + g]));
     }
     return y;
 }
-// Their weights 2^(y - rc) as FP16 pairs; returns the sum of weight / vs.
-template <bool EDGE>
-__device__ __forceinline__ float chunk_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, uint32_t ch, float rowf,
-                                               float rc, int end, uint32_t (&pk)[16]) {
-    float sum = 0.f;
+// Their weights 2^(y - rc) as FP16 pairs; returns l + the sum of weight / vs.
+__device__ __forceinline__ float score_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf, float rc,
+                                               float l, uint32_t (&pk)[16]) {
+    const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
-    for (uint32_t g = 0; g < 2; ++g) {
+    for (int g = 0; g < 2; ++g) {
         const float f = tl->ks[at][2 * ch + g] * rowf, d = tl->lv[at][2 * ch + g] - rc;
         const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(d, d);
         uint64_t s2 = pack_f32x2(0.f, 0.f);
-        const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-            float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1])), ff, dd));
-            if (EDGE) {
-                const int k = 32 * static_cast<int>(ch) + 16 * static_cast<int>(g) + e;
-                if (k >= end) y.x = -INFINITY;
-                if (k + 1 >= end) y.y = -INFINITY;
-            }
+            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1])), ff, dd));
             const float a = ex2(y.x), b = ex2(y.y);
             s2 = fma_f32x2(pack_f32x2(a, b), one, s2);
             pk[8 * g + e / 2] = pack2<true>(a, b);
         }
         const float2 s = unpack_f32x2(s2);
-        sum = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], sum);
+        l = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], l);
     }
-    return sum;
+    return l;
+}
+
+// NaN values of the keys [lo, hi), which the products at the causal edge left out, marked
+// in the outputs (or this range's part of them) of a row that sees these keys.
+__device__ __noinline__ void mark_nan(const AttnArgs& p, uint32_t b, uint32_t h, int lo, int hi, uint16_t* dst, float* part) {
+    for (int key = lo; key < hi; ++key) {
+        const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
+        if (page < 0 || page >= static_cast<int>(p.c.num_pages)) continue;
+        const uint8_t* v = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(page) * p.c.page_stride +
+                           static_cast<int64_t>(h) * p.c.head_stride +
+                           static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
+        for (uint32_t d = 0; d < p.c.head_dim; ++d)
+            if ((v[d] & 0x7F) == 0x7F) {
+                if (dst) dst[d] = 0x7FC0u;   // a NaN in BF16 and in FP16
+                else part[d * kItemRows] = __uint_as_float(0x7FC00000u);
+            }
+    }
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -385,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     {
                         float mx = 0.f;
                         bool bad = false;
-#pragma unroll 4
+#pragma unroll 2
                         for (uint32_t d = 0; d < DP; d += 8) {
                             uint4 a = make_uint4(0, 0, 0, 0);
                             if (real && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
@@ -398,8 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                             }
                         }
                         const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
-                        rowf = rs.scale;
-#pragma unroll 4
+                        // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
+                        rowf = bad ? rs.scale : fmaxf(rs.scale, 1.3552527156068805e-20f);
+#pragma unroll 2
                         for (uint32_t d = 0; d < DP; d += 8) {
                             uint4 a = make_uint4(0, 0, 0, 0);
                             if (real && !bad && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
@@ -431,50 +451,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         const uint32_t at = (unit0 + j) % kScaleRing;
                         const int key0 = static_cast<int>((j0 + j) * kTile);
                         const bool edge = key0 + static_cast<int>(kTile) > warp_min;
-                        // ---- the unit's maximum, against which `ref` is good enough or moves
-                        float ymax = -INFINITY;
-                        uint32_t v[2][32];
-                        tmem_ld32(tS, v[0]);
-#pragma unroll 1
-                        for (uint32_t ch = 0; ch < 4; ch += 2)
+                        // ---- the row's 128 scores, and the maximum of y = score ks rowf + log2(vs)
+                        // (columns 96-127 are read first, and again at the end: 96 registers hold the rest)
+                        uint32_t v[3][32], w[32];
+                        const int end = edge ? row_end - key0 : static_cast<int>(kTile);
+                        tmem_ld32(tS + 96, w);
+                        tc_wait_ld();
 #pragma unroll
-                            for (uint32_t half = 0; half < 2; ++half) {
-                                tc_wait_ld();
-                                // (after the last chunk: the first again, for the pass below)
-                                tmem_ld32(tS + 32 * ((ch + half + 1) % 4), v[half ^ 1]);
-                                ymax = fmaxf(ymax, edge ? chunk_max<true>(v[half], tl, at, ch + half, rowf, row_end - key0)
-                                                        : chunk_max<false>(v[half], tl, at, ch + half, rowf, 0));
-                            }
+                        for (int ch = 0; ch < 3; ++ch) tmem_ld32(tS + 32 * ch, v[ch]);
+                        if (edge) mask_scores(w, 96, end);
+                        float ymax = score_max(w, tl, at, 3, rowf);
+                        tc_wait_ld();
+                        if (edge) {
+#pragma unroll
+                            for (int ch = 0; ch < 3; ++ch) mask_scores(v[ch], 32 * ch, end);
+                        }
+#pragma unroll
+                        for (int ch = 0; ch < 3; ++ch) ymax = fmaxf(ymax, score_max(v[ch], tl, at, ch, rowf));
                         if (__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) {
                             const float m_new = fmaxf(ref, ymax);
                             const float a = ref == -INFINITY ? 0.f : ex2(ref - m_new);
                             l *= a;
                             ref = m_new;
                             if (j > 0) {
-                                tc_wait_ld();
 #pragma unroll 1
-                                for (uint32_t d = 0; d < DP; d += 32) {
-                                    tmem_ld32(tO + d, v[1]);
+                                for (uint32_t d = 0; d < DP; d += 8) {
+                                    float o[8];
+                                    tmem_ld_32x32b_x8(tO + d, o);
                                     tc_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) v[1][e] = __float_as_uint(__uint_as_float(v[1][e]) * a);
-                                    tmem_st_32x32b_x32(tO + d, v[1]);
+                                    tmem_st8(tO + d, o, a);
                                 }
                             }
                         }
-                        // ---- P, over the columns of S that have been read
+                        // ---- P, over the columns of S
                         const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
-#pragma unroll 1
-                        for (uint32_t ch = 0; ch < 4; ch += 2)
+                        tmem_ld32(tS + 96, w);
 #pragma unroll
-                            for (uint32_t half = 0; half < 2; ++half) {
-                                tc_wait_ld();
-                                if (ch + half < 3) tmem_ld32(tS + 32 * (ch + half + 1), v[half ^ 1]);
-                                uint32_t pk[16];
-                                l += edge ? chunk_weights<true>(v[half], tl, at, ch + half, rowf, rc, row_end - key0, pk)
-                                          : chunk_weights<false>(v[half], tl, at, ch + half, rowf, rc, 0, pk);
-                                tmem_st_32x32b_x16(tS + 16 * (ch + half), pk);
-                            }
+                        for (int ch = 0; ch < 3; ++ch) {
+                            uint32_t pk[16];
+                            l = score_weights(v[ch], tl, at, ch, rowf, rc, l, pk);
+                            tmem_st_32x32b_x16(tS + 16 * ch, pk);
+                        }
+                        tc_wait_ld();
+                        if (edge) mask_scores(w, 96, end);
+                        {
+                            uint32_t pk[16];
+                            l = score_weights(w, tl, at, 3, rowf, rc, l, pk);
+                            tmem_st_32x32b_x16(tS + 48, pk);
+                        }
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
@@ -499,27 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(tok)) * p.out.token_stride +
                                     static_cast<int64_t>(head) * p.out.head_stride;
-                    const bool poisoned = *static_cast<volatile int*>(&tl->nan_seen) != 0;
 #pragma unroll 1
                     for (uint32_t d = 0; d < DP; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(tO + d, o);
                         tc_wait_ld();
-                        if (poisoned && real) {
-                            // NaN values left out of the products at the causal edge: the rows that see them
-                            const int lo = max(static_cast<int>(j0 * kTile), (it.s.len - it.s.count + static_cast<int>(it.rb * kItemRows / p.group) + 1) / static_cast<int>(kTile) * static_cast<int>(kTile));
-                            const int hi = min(row_end, static_cast<int>((j0 + cnt) * kTile));
-                            for (int key = lo; key < hi; ++key) {
-                                const int page = p.b.page_table[static_cast<int64_t>(it.b) * p.b.page_table_stride + (key >> p.page_shift)];
-                                if (page < 0 || page >= static_cast<int>(p.c.num_pages)) continue;
-                                const uint8_t* vp = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(page) * p.c.page_stride +
-                                                    static_cast<int64_t>(it.h) * p.c.head_stride +
-                                                    static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (d + e < p.c.head_dim && (vp[d + e] & 0x7F) == 0x7F) o[e] = 0x7FC00000u;
-                            }
-                        }
                         if (whole) {
                             if (real) {
 #pragma unroll
@@ -540,6 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         slot[DP * kItemRows + t * kTile + row] = ref;
                         slot[(DP + 1) * kItemRows + t * kTile + row] = l;
                     }
+                    if (*static_cast<volatile int*>(&tl->nan_seen) != 0 && real)
+                        mark_nan(p, it.b, it.h,
+                                 max(static_cast<int>(j0 * kTile), edge_key(it.s, p.group, it.rb) / static_cast<int>(kTile) * static_cast<int>(kTile)),
+                                 min(row_end, static_cast<int>((j0 + cnt) * kTile)), whole ? dst : nullptr, slot + t * kTile + row);
                 } else if (issuer) {
                     // an item without this tile: its stages are released as they come
                     for (uint32_t j = 0; j < cnt && ok; ++j) {
@@ -562,8 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             }
         } else {
             // --------------------------------------------- codes -> FP16 tiles
-            constexpr uint32_t CH = DP / 16, kRowsPass = 128 / CH;   // 16-code chunks of a row; rows per pass
-            const uint32_t ct = threadIdx.x - 32 * kSoftmaxWarps, ch = ct % CH, r0 = ct / CH;
+            // A warp takes 32 keys, 8 rows x 4 chunks of 16 codes at a time: 64 contiguous bytes a
+            // row from memory, and the eight lanes of a store phase hold one unit of eight rows,
+            // which the swizzle spreads over all banks.
+            constexpr uint32_t CH = DP / 16, kHalves = DP / 64;
+            const uint32_t cw = warp - kSoftmaxWarps, lrow = lane & 7, lch = lane >> 3;
+            const uint32_t st0 = (cw * 32 + lrow) * 128 + (((2 * lch) ^ lrow) << 4), st1 = (cw * 32 + lrow) * 128 + (((2 * lch + 1) ^ lrow) << 4);
             struct Unit {
                 int key0, end;
                 bool edge;
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                 if (un >= it.first + it.n) next_item(p, it);
                 x.key0 = static_cast<int>(un - it.first) * static_cast<int>(kTile);
                 x.end = block_end(it.s, p.group, it.rb);
-                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > it.s.len - it.s.count + static_cast<int>(it.rb * kItemRows / p.group) + 1;
+                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > edge_key(it.s, p.group, it.rb);
                 x.b = it.b;
                 x.h = it.h;
                 ++un;
@@ -583,11 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             };
             // lane l < 8: page and scales of keys [16 l, 16 l + 16) of a unit
             int page = -1;
-            float mk = 0.f, mv = 1.f;
+            float mk = 1.f, mv = 1.f;
             const auto load_meta = [&](const Unit& x) {
                 page = -1;
-                mk = 0.f;
-                mv = 1.f;
+                mk = mv = 1.f;
                 const int key = x.key0 + 16 * static_cast<int>(lane);
                 if (lane < 8 && key < x.end) {
                     const int pg = p.b.page_table[static_cast<int64_t>(x.b) * p.b.page_table_stride + (key >> p.page_shift)];
@@ -598,73 +613,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         page = pg;
                         mk = p.c.k_scale[s];
                         mv = p.c.v_scale[s];
+                        if (mk < kMinScale) mk = kMinScale;
                         if (mv < kMinScale) mv = kMinScale;
                     }
                 }
             };
             const auto load_codes = [&](const Unit& x, const void* codes, uint4 (&q)[CH]) {
+                const uint8_t* base[2];   // this lane's first chunk of the warp's two groups of 16 keys
+                int left[2];              // keys of the group that exist
+#pragma unroll
+                for (uint32_t g = 0; g < 2; ++g) {
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, 2 * cw + g);
+                    const int key = x.key0 + static_cast<int>(32 * cw + 16 * g);
+                    base[g] = static_cast<const uint8_t*>(codes) + static_cast<int64_t>(max(pg, 0)) * p.c.page_stride +
+                              static_cast<int64_t>(x.h) * p.c.head_stride +
+                              static_cast<int64_t>((key & static_cast<int>(p.c.page_size - 1)) + static_cast<int>(lrow)) * p.c.token_stride + 16 * lch;
+                    left[g] = pg < 0 ? 0 : x.end - key;
+                }
 #pragma unroll
                 for (uint32_t i = 0; i < CH; ++i) {
-                    const uint32_t r = i * kRowsPass + r0;
-                    const int key = x.key0 + static_cast<int>(r);
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r >> 4);
+                    const uint32_t g = i / (2 * kHalves), r8 = i / kHalves % 2, half = i % kHalves;
                     q[i] = make_uint4(0, 0, 0, 0);
-                    if (pg >= 0 && key < x.end && 16 * ch < p.c.head_dim)
-                        q[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + static_cast<int64_t>(pg) * p.c.page_stride +
-                                                                    static_cast<int64_t>(x.h) * p.c.head_stride +
-                                                                    static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride +
-                                                                    16 * ch);
+                    if (static_cast<int>(8 * r8 + lrow) < left[g] && 64 * half + 16 * lch < p.c.head_dim)
+                        q[i] = *reinterpret_cast<const uint4*>(base[g] + static_cast<int64_t>(8 * r8) * p.c.token_stride + 64 * half);
                 }
             };
-            const auto store_tile = [&](uint32_t tile, const uint4 (&q)[CH], bool clean) {
-                uint32_t any = 0;
+            const auto store_tile = [&](uint32_t tile, uint4 (&q)[CH], bool clean) {
+                if (clean) {   // NaN values at the causal edge: 0 here, marked at the end (mark_nan)
+                    uint32_t any = 0;
+#pragma unroll
+                    for (uint32_t i = 0; i < CH; ++i) {
+                        q[i].x = drop_nan(q[i].x, any);
+                        q[i].y = drop_nan(q[i].y, any);
+                        q[i].z = drop_nan(q[i].z, any);
+                        q[i].w = drop_nan(q[i].w, any);
+                    }
+                    if (any) *static_cast<volatile int*>(&tl->nan_seen) = 1;
+                }
 #pragma unroll
                 for (uint32_t i = 0; i < CH; ++i) {
-                    const uint32_t r = i * kRowsPass + r0;
-                    uint4 c = q[i], lo, hi;
-                    if (clean) {
-                        c.x = drop_nan(c.x, any);
-                        c.y = drop_nan(c.y, any);
-                        c.z = drop_nan(c.z, any);
-                        c.w = drop_nan(c.w, any);
-                    }
-                    convert16(c, lo, hi);
-                    uint8_t* at = smem + tile + (ch / 4) * C::kHalfBytes + r * 128;
-                    const uint32_t un0 = (2 * ch) % 8;
-                    // the chunks of the second half store their halves in the other order: no bank is hit twice
-                    const bool swap = ch >= 4;
-                    *reinterpret_cast<uint4*>(at + (((un0 + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? hi : lo;
-                    *reinterpret_cast<uint4*>(at + (((un0 + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                    uint4 lo, hi;
+                    convert16(q[i], lo, hi);
+                    uint8_t* at = smem + tile + (i % kHalves) * C::kHalfBytes + i / kHalves * 1024;
+                    *reinterpret_cast<uint4*>(at + st0) = lo;
+                    *reinterpret_cast<uint4*>(at + st1) = hi;
                 }
-                if (any) *static_cast<volatile int*>(&tl->nan_seen) = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
             };
+            // step i: store unit i (its codes in registers), load unit i + 1's, look unit i + 2's pages up
             Unit cur{}, ahead{};
             uint4 kq[CH], vq[CH];
-            bool have = next_unit(cur);
-            load_meta(cur);
-            load_codes(cur, p.c.k_codes, kq);
-            load_codes(cur, p.c.v_codes, vq);
-            float sk = mk, sv = mv;
-            bool more = next_unit(ahead);
-            if (more) load_meta(ahead);
-            for (uint32_t i = 0; have; ++i) {
+            float sk = 1.f, sv = 1.f;
+            bool have = false, more = next_unit(ahead);
+            load_meta(ahead);
+#pragma unroll 1
+            for (uint32_t i = 0xFFFFFFFFu; have || more; ++i) {
                 const uint32_t st = i % kStages, parity = ((i / kStages) & 1) ^ 1;
-                if (!wait_warp(smem_u32(&tl->kempty[st]), parity, tmo, abort_flag, kWaitKFree)) break;
-                store_tile(C::kK + st * C::kTileBytes, kq, false);
-                // Slot i % 4 is free: unit i - 4 was read before unit i - 2's products could free this K stage
-                if (warp == kSoftmaxWarps && lane < 8) {
-                    tl->ks[i % kScaleRing][lane] = sk;
-                    tl->lv[i % kScaleRing][lane] = __log2f(sv);
-                    tl->iv[i % kScaleRing][lane] = __frcp_rn(sv);
+                if (have) {
+                    if (!wait_warp(smem_u32(&tl->kempty[st]), parity, tmo, abort_flag, kWaitKFree)) break;
+                    store_tile(C::kK + st * C::kTileBytes, kq, false);
+                    // Slot i % 4 is free: unit i - 4 was read before unit i - 2's products could free this K stage
+                    if (warp == kSoftmaxWarps && lane < 8) {
+                        tl->ks[i % kScaleRing][lane] = sk;
+                        tl->lv[i % kScaleRing][lane] = __log2f(sv);
+                        tl->iv[i % kScaleRing][lane] = __frcp_rn(sv);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&tl->kfull[st]));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&tl->kfull[st]));
                 if (more) load_codes(ahead, p.c.k_codes, kq);
-                if (!wait_warp(smem_u32(&tl->vempty[st]), parity, tmo, abort_flag, kWaitVFree)) break;
-                store_tile(C::kV + st * C::kTileBytes, vq, cur.edge);
-                if (lane == 0) mbar_arrive(smem_u32(&tl->vfull[st]));
+                if (have) {
+                    if (!wait_warp(smem_u32(&tl->vempty[st]), parity, tmo, abort_flag, kWaitVFree)) break;
+                    store_tile(C::kV + st * C::kTileBytes, vq, cur.edge);
+                    if (lane == 0) mbar_arrive(smem_u32(&tl->vfull[st]));
+                }
                 have = more;
                 if (more) {
                     load_codes(ahead, p.c.v_codes, vq);
