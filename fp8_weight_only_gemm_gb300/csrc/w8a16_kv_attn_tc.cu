@@ -14,9 +14,10 @@
 // thread of each issues the tile's products, S = Q K^T (M = 128 rows, N = 128 keys) and
 // O += P V with P read from TMEM, so one tile's softmax runs under the other's products
 // (an issuing warp of its own would be a 13th, and leave 128 registers a thread instead of
-// 168). A thread owns a row, so no reduction crosses threads: it reads its
-// 128 scores from TMEM, and only where a unit's maximum exceeds the running one by more than
-// 8 is that moved and O rescaled; P (at most 2^15, FP16) overwrites the columns of S.
+// 168). A thread owns a row, so no reduction crosses threads: a pass over its 128
+// scores in TMEM forms P (at most 2^15, FP16) in registers against the running maximum of the
+// units before; only where a row's maximum has risen by more than 2^8 is the maximum moved, O
+// rescaled and the pass repeated. P then overwrites the first columns of S.
 //
 // TMEM: S/P of the tiles at columns 0 and 128, O at 256 and 256 + DP.
 #include <cuda_runtime.h>
@@ -114,23 +115,31 @@ __device__ __forceinline__ void next_item(const AttnArgs& p, Item& it) {
     }
     it.n = block_units(it.s, p.group, it.rb);
 }
+// Leaves the counts of the first kChunk sequences in sh.
 template <uint32_t WARPS>
 __device__ __noinline__ uint64_t total_units(const AttnArgs& p, uint64_t* sh, bool report) {
     uint64_t n = 0;
-    for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
+    for (uint32_t b0 = (p.b.batch - 1) / kChunk * kChunk;; b0 -= kChunk) {
         const uint32_t count = chunk_units<WARPS>(p, b0, sh, report);
-        for (uint32_t i = 0; i < count; ++i) n += sh[i];
+        uint64_t x = 0;   // a warp's lanes share the sum
+        for (uint32_t i = threadIdx.x & 31; i < count; i += 32) x += sh[i];
+        n += warp_sum(x);
+        if (b0 == 0) break;
         __syncthreads();
     }
     return n * p.c.kv_heads;
 }
-// The item that holds unit u (below the total).
+// The item that holds unit u (below the total); sh as total_units left it.
 template <uint32_t WARPS>
 __device__ __noinline__ Item find_item(const AttnArgs& p, uint64_t u, uint64_t* sh) {
     Item it{};
     uint64_t base = 0;
     for (uint32_t b0 = 0; b0 < p.b.batch; b0 += kChunk) {
-        const uint32_t count = chunk_units<WARPS>(p, b0, sh, false);
+        if (b0) {
+            __syncthreads();
+            chunk_units<WARPS>(p, b0, sh, false);
+        }
+        const uint32_t count = min(kChunk, p.b.batch - b0);
         for (uint32_t i = 0; i < count; ++i) {
             const uint64_t n = sh[i] * p.c.kv_heads;
             if (u < base + n) {
@@ -138,17 +147,28 @@ __device__ __noinline__ Item find_item(const AttnArgs& p, uint64_t u, uint64_t* 
                 it.b = b0 + i;
                 it.h = static_cast<uint32_t>((u - base) / sh[i]);
                 uint64_t rest = (u - base) % sh[i];
-                while (rest >= (it.n = block_units(it.s, p.group, it.rb))) {
-                    rest -= it.n;
-                    ++it.rb;
+                const uint32_t lane = threadIdx.x & 31, nb = seq_blocks(it.s, p.group);
+                for (uint32_t r0 = 0;; r0 += 32) {   // the row block that holds it, 32 at a time
+                    const uint32_t mine = r0 + lane < nb ? block_units(it.s, p.group, r0 + lane) : 0u;
+                    uint64_t inc = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint64_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                        if (lane >= static_cast<uint32_t>(o)) inc += x;
+                    }
+                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rest < inc);
+                    if (hit) {
+                        const int at = __ffs(hit) - 1;
+                        it.rb = r0 + at;
+                        it.n = __shfl_sync(0xFFFFFFFFu, mine, at);
+                        it.first = u - (rest - (__shfl_sync(0xFFFFFFFFu, inc, at) - it.n));
+                        return it;
+                    }
+                    rest -= __shfl_sync(0xFFFFFFFFu, inc, 31);
                 }
-                it.first = u - rest;
-                __syncthreads();
-                return it;
             }
             base += n;
         }
-        __syncthreads();
     }
     return it;
 }
@@ -233,38 +253,30 @@ __device__ __forceinline__ void mask_scores(uint32_t (&v)[32], int first, int en
     for (int e = 0; e < 32; ++e)
         if (first + e >= end) v[e] = 0xFF800000u;
 }
-// Their largest y = score ks rowf + log2(vs) (ks rowf > 0: the largest score gives the largest y).
-__device__ __forceinline__ float score_max(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf) {
-    float y = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) mx = max3(mx, __uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1]));
-        y = fmaxf(y, fmaf(mx, tl->ks[at][2 * ch + g] * rowf, tl->lv[at][2 * ch + g]));
-    }
-    return y;
-}
-// Their weights 2^(y - rc) as FP16 pairs; returns l + the sum of weight / vs.
-__device__ __forceinline__ float score_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf, float rc,
-                                               float l, uint32_t (&pk)[16]) {
+// Their weights 2^(y - rc) as FP16 pairs, y = score ks rowf + log2(vs); the largest y
+// (ks rowf > 0: that of the largest score) and the sum of weight / vs are added to.
+__device__ __forceinline__ void score_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf, float rc,
+                                              float& ymax, float& lsum, uint32_t (&pk)[16]) {
     const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        const float f = tl->ks[at][2 * ch + g] * rowf, d = tl->lv[at][2 * ch + g] - rc;
-        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(d, d);
+        const float f = tl->ks[at][2 * ch + g] * rowf, lv = tl->lv[at][2 * ch + g];
+        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(lv - rc, lv - rc);
         uint64_t s2 = pack_f32x2(0.f, 0.f);
+        float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1])), ff, dd));
+            const float x0 = __uint_as_float(v[16 * g + e]), x1 = __uint_as_float(v[16 * g + e + 1]);
+            mx = max3(mx, x0, x1);
+            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(x0, x1), ff, dd));
             const float a = ex2(y.x), b = ex2(y.y);
             s2 = fma_f32x2(pack_f32x2(a, b), one, s2);
             pk[8 * g + e / 2] = pack2<true>(a, b);
         }
+        ymax = fmaxf(ymax, fmaf(mx, f, lv));
         const float2 s = unpack_f32x2(s2);
-        l = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], l);
+        lsum = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], lsum);
     }
-    return l;
 }
 
 // NaN values of the keys [lo, hi), which the products at the causal edge left out, marked
@@ -402,35 +414,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                                           static_cast<int64_t>(head) * p.q.head_stride;
                     float rowf;
                     {
-                        float mx = 0.f;
-                        bool bad = false;
-#pragma unroll 2
+                        uint32_t w[DP / 2];   // the whole row: its loads are in flight together
+#pragma unroll
                         for (uint32_t d = 0; d < DP; d += 8) {
                             uint4 a = make_uint4(0, 0, 0, 0);
                             if (real && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
-                            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                            w[d / 2] = a.x, w[d / 2 + 1] = a.y, w[d / 2 + 2] = a.z, w[d / 2 + 3] = a.w;
+                        }
+                        float mx = 0.f;
+                        bool bad = false;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 x = unpack2<F16>(w[e]);
-                                bad = bad || !(fabsf(x.x) <= 3.4028235e38f) || !(fabsf(x.y) <= 3.4028235e38f);
-                                mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
-                            }
+                        for (uint32_t e = 0; e < DP / 2; ++e) {
+                            const float2 x = unpack2<F16>(w[e]);
+                            bad = bad || !(fabsf(x.x) <= 3.4028235e38f) || !(fabsf(x.y) <= 3.4028235e38f);
+                            mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
                         }
                         const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
                         // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
                         rowf = bad ? rs.scale : fmaxf(rs.scale, 1.3552527156068805e-20f);
-#pragma unroll 2
-                        for (uint32_t d = 0; d < DP; d += 8) {
-                            uint4 a = make_uint4(0, 0, 0, 0);
-                            if (real && !bad && d < p.c.head_dim) a = *reinterpret_cast<const uint4*>(src + d);
-                            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (uint32_t un = 0; un < DP / 8; ++un) {
                             uint32_t o[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float2 x = unpack2<F16>(w[e]);
-                                o[e] = pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
+                                const float2 x = unpack2<F16>(w[4 * un + e]);
+                                o[e] = bad ? 0u : pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
                             }
-                            const uint32_t un = d / 8;
                             *reinterpret_cast<uint4*>(smem + C::kQ + t * C::kTileBytes + (un / 8) * C::kHalfBytes + row * 128 +
                                                       (((un % 8) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
@@ -451,24 +460,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         const uint32_t at = (unit0 + j) % kScaleRing;
                         const int key0 = static_cast<int>((j0 + j) * kTile);
                         const bool edge = key0 + static_cast<int>(kTile) > warp_min;
-                        // ---- the row's 128 scores, and the maximum of y = score ks rowf + log2(vs)
-                        // (columns 96-127 are read first, and again at the end: 96 registers hold the rest)
-                        uint32_t v[3][32], w[32];
+                        // ---- P against the maximum of the units before; again, where the unit's own is far above it
                         const int end = edge ? row_end - key0 : static_cast<int>(kTile);
-                        tmem_ld32(tS + 96, w);
-                        tc_wait_ld();
+                        uint32_t pk[4][16];
+                        float lsum;
+#pragma unroll 1
+                        for (int pass = 0; pass < 2; ++pass) {
+                            const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
+                            float ymax = -INFINITY;
+                            lsum = 0.f;
+                            uint32_t v[2][32];
+                            tmem_ld32(tS, v[0]);
 #pragma unroll
-                        for (int ch = 0; ch < 3; ++ch) tmem_ld32(tS + 32 * ch, v[ch]);
-                        if (edge) mask_scores(w, 96, end);
-                        float ymax = score_max(w, tl, at, 3, rowf);
-                        tc_wait_ld();
-                        if (edge) {
-#pragma unroll
-                            for (int ch = 0; ch < 3; ++ch) mask_scores(v[ch], 32 * ch, end);
-                        }
-#pragma unroll
-                        for (int ch = 0; ch < 3; ++ch) ymax = fmaxf(ymax, score_max(v[ch], tl, at, ch, rowf));
-                        if (__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) {
+                            for (int ch = 0; ch < 4; ++ch) {
+                                tc_wait_ld();
+                                if (ch < 3) tmem_ld32(tS + 32 * (ch + 1), v[(ch + 1) & 1]);
+                                if (edge) mask_scores(v[ch & 1], 32 * ch, end);
+                                score_weights(v[ch & 1], tl, at, ch, rowf, rc, ymax, lsum, pk[ch]);
+                            }
+                            if (!__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) break;
                             const float m_new = fmaxf(ref, ymax);
                             const float a = ref == -INFINITY ? 0.f : ex2(ref - m_new);
                             l *= a;
@@ -483,22 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                                 }
                             }
                         }
-                        // ---- P, over the columns of S
-                        const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
-                        tmem_ld32(tS + 96, w);
+                        l += lsum;
 #pragma unroll
-                        for (int ch = 0; ch < 3; ++ch) {
-                            uint32_t pk[16];
-                            l = score_weights(v[ch], tl, at, ch, rowf, rc, l, pk);
-                            tmem_st_32x32b_x16(tS + 16 * ch, pk);
-                        }
-                        tc_wait_ld();
-                        if (edge) mask_scores(w, 96, end);
-                        {
-                            uint32_t pk[16];
-                            l = score_weights(w, tl, at, 3, rowf, rc, l, pk);
-                            tmem_st_32x32b_x16(tS + 48, pk);
-                        }
+                        for (int ch = 0; ch < 4; ++ch) tmem_st_32x32b_x16(tS + 16 * ch, pk[ch]);
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
