@@ -366,16 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
             uint32_t blocks = 0, items = 0;   // units and items of this tile
             bool first_part = true, ok = true;
+            const uint64_t desc_q = smem_desc_kmajor_sw128(sbase + C::kQ + t * C::kTileBytes), desc_k = smem_desc_kmajor_sw128(sbase + C::kK),
+                           desc_v = smem_desc_mn_sw128(sbase + C::kV, C::kHalfBytes);
             // (issuer) S of the CTA's unit i, once its K tile is there
             const auto scores = [&](uint32_t i) {
                 const uint32_t st = i % kStages;
                 if (!wait_one(smem_u32(&tl->kfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitK)) return false;
                 tc_fence_after();
+                const uint64_t k0 = desc_k + st * (C::kTileBytes >> 4);   // descriptors count 16 bytes
 #pragma unroll
                 for (uint32_t k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = (k / 4) * C::kHalfBytes + (k % 4) * 32;
-                    mma_ss(tm + t * kTile, smem_desc_kmajor_sw128(sbase + C::kQ + t * C::kTileBytes + off),
-                           smem_desc_kmajor_sw128(sbase + C::kK + st * C::kTileBytes + off), idS, k > 0);
+                    const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
+                    mma_ss(tm + t * kTile, desc_q + off, k0 + off, idS, k > 0);
                 }
                 tc_commit(smem_u32(&tl->sfull[t]));
                 mbar_arrive(smem_u32(&tl->sfull[t]));
@@ -389,10 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     !wait_one(smem_u32(&tl->vfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitV))
                     return false;
                 tc_fence_after();
+                const uint64_t v0 = desc_v + st * (C::kTileBytes >> 4);
 #pragma unroll
                 for (uint32_t k = 0; k < kTile / 16; ++k)
-                    tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + 8 * k,
-                                  smem_desc_mn_sw128(sbase + C::kV + st * C::kTileBytes + k * 2048, C::kHalfBytes), idO, add || k > 0);
+                    tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
                 tc_commit(smem_u32(&tl->vempty[st]));
                 return true;
             };
@@ -517,7 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     // ---- outputs, or this range's part of them ([d][row], coalesced over rows)
                     const bool whole = cnt == it.n;
                     float* slot = p.ws + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * ((DP + 2) * kItemRows);
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const bool none = l == 0.f;   // a row that sees no key is zero
+                    const float inv = none ? 0.f : 1.f / l;
+                    const auto norm = [&](uint32_t x) { return __uint_as_float(x) * inv; };
                     uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(tok)) * p.out.token_stride +
                                     static_cast<int64_t>(head) * p.out.head_stride;
 #pragma unroll 1
@@ -525,16 +529,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         uint32_t o[32];
                         tmem_ld32(tO + d, o);
                         tc_wait_ld();
+                        if (none) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        }
                         if (whole) {
                             if (real) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 8)
                                     if (d + e < p.c.head_dim)
                                         *reinterpret_cast<uint4*>(dst + d + e) =
-                                            make_uint4(pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
-                                                       pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
-                                                       pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
-                                                       pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+                                            make_uint4(pack2<F16>(norm(o[e]), norm(o[e + 1])),
+                                                       pack2<F16>(norm(o[e + 2]), norm(o[e + 3])),
+                                                       pack2<F16>(norm(o[e + 4]), norm(o[e + 5])),
+                                                       pack2<F16>(norm(o[e + 6]), norm(o[e + 7])));
                             }
                         } else {
 #pragma unroll
@@ -576,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             // which the swizzle spreads over all banks.
             constexpr uint32_t CH = DP / 16, kHalves = DP / 64;
             const uint32_t cw = warp - kSoftmaxWarps, lrow = lane & 7, lch = lane >> 3;
+            const uint32_t off0 = min(16 * lch, p.c.head_dim - 16), off1 = min(64 + 16 * lch, p.c.head_dim - 16);
             const uint32_t st0 = (cw * 32 + lrow) * 128 + (((2 * lch) ^ lrow) << 4), st1 = (cw * 32 + lrow) * 128 + (((2 * lch + 1) ^ lrow) << 4);
             struct Unit {
                 int key0, end;
@@ -583,12 +592,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                 uint32_t b, h;
             };
             uint64_t un = u0;   // next unit to look up
+            int it_end = block_end(it.s, p.group, it.rb), it_edge = edge_key(it.s, p.group, it.rb);
             const auto next_unit = [&](Unit& x) {
                 if (un >= u_end) return false;
-                if (un >= it.first + it.n) next_item(p, it);
+                if (un >= it.first + it.n) {
+                    next_item(p, it);
+                    it_end = block_end(it.s, p.group, it.rb);
+                    it_edge = edge_key(it.s, p.group, it.rb);
+                }
                 x.key0 = static_cast<int>(un - it.first) * static_cast<int>(kTile);
-                x.end = block_end(it.s, p.group, it.rb);
-                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > edge_key(it.s, p.group, it.rb);
+                x.end = it_end;
+                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > it_edge;
                 x.b = it.b;
                 x.h = it.h;
                 ++un;
@@ -615,25 +629,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     }
                 }
             };
+            // Rows past the last key, and chunks past the head, repeat the last ones: their scores are
+            // masked and their queries and outputs are not there, and their values are as finite as
+            // those that they repeat (in a unit where rows see different keys: after drop_nan).
             const auto load_codes = [&](const Unit& x, const void* codes, uint4 (&q)[CH]) {
-                const uint8_t* base[2];   // this lane's first chunk of the warp's two groups of 16 keys
-                int left[2];              // keys of the group that exist
+                const uint8_t* row[4];   // this lane's rows of 8
+                const int last = max(x.end - 1 - x.key0, 0);
 #pragma unroll
-                for (uint32_t g = 0; g < 2; ++g) {
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, 2 * cw + g);
-                    const int key = x.key0 + static_cast<int>(32 * cw + 16 * g);
-                    base[g] = static_cast<const uint8_t*>(codes) + static_cast<int64_t>(max(pg, 0)) * p.c.page_stride +
-                              static_cast<int64_t>(x.h) * p.c.head_stride +
-                              static_cast<int64_t>((key & static_cast<int>(p.c.page_size - 1)) + static_cast<int>(lrow)) * p.c.token_stride + 16 * lch;
-                    left[g] = pg < 0 ? 0 : x.end - key;
+                for (uint32_t i = 0; i < 4; ++i) {
+                    const int r = min(static_cast<int>(32 * cw + 8 * i + lrow), last);
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r >> 4);
+                    row[i] = static_cast<const uint8_t*>(codes) + static_cast<int64_t>(max(pg, 0)) * p.c.page_stride +
+                             static_cast<int64_t>(x.h) * p.c.head_stride +
+                             static_cast<int64_t>((x.key0 + r) & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
                 }
 #pragma unroll
-                for (uint32_t i = 0; i < CH; ++i) {
-                    const uint32_t g = i / (2 * kHalves), r8 = i / kHalves % 2, half = i % kHalves;
-                    q[i] = make_uint4(0, 0, 0, 0);
-                    if (static_cast<int>(8 * r8 + lrow) < left[g] && 64 * half + 16 * lch < p.c.head_dim)
-                        q[i] = *reinterpret_cast<const uint4*>(base[g] + static_cast<int64_t>(8 * r8) * p.c.token_stride + 64 * half);
-                }
+                for (uint32_t i = 0; i < CH; ++i)
+                    q[i] = *reinterpret_cast<const uint4*>(row[i / kHalves] + (i % kHalves ? off1 : off0));
             };
             const auto store_tile = [&](uint32_t tile, uint4 (&q)[CH], bool clean) {
                 if (clean) {   // NaN values at the causal edge: 0 here, marked at the end (mark_nan)
