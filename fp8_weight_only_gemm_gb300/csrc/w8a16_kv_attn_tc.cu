@@ -52,7 +52,7 @@ struct Cfg {
     static constexpr uint32_t kSmem = 1024 + kTail + 1024;
 };
 struct Tail {
-    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2], odone[2], drain[2];
+    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2], odone[2], drain[2], turn[2];
     uint32_t tmem;
     int abort_flag;
     int nan_seen;
@@ -60,7 +60,7 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= 1024, "barrier block");
 
-enum Wait : unsigned { kWaitQ = 1, kWaitK, kWaitV, kWaitKFree, kWaitVFree, kWaitS, kWaitP, kWaitO, kWaitDrain };
+enum Wait : unsigned { kWaitQ = 1, kWaitK, kWaitV, kWaitKFree, kWaitVFree, kWaitS, kWaitP, kWaitO, kWaitDrain, kWaitTurn };
 
 // ------------------------------------------------------------ the schedule --
 // Keys that the last row of row block rb sees, and the units of its item.
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                 mbar_init(smem_u32(&tl->pfull[i]), 4);
                 mbar_init(smem_u32(&tl->odone[i]), 2);
                 mbar_init(smem_u32(&tl->drain[i]), 1);
+                mbar_init(smem_u32(&tl->turn[i]), 1);
             }
             tl->abort_flag = 0;
             tl->nan_seen = 0;
@@ -368,11 +369,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             bool first_part = true, ok = true;
             const uint64_t desc_q = smem_desc_kmajor_sw128(sbase + C::kQ + t * C::kTileBytes), desc_k = smem_desc_kmajor_sw128(sbase + C::kK),
                            desc_v = smem_desc_mn_sw128(sbase + C::kV, C::kHalfBytes);
-            // (issuer) S of the CTA's unit i, once its K tile is there
-            const auto scores = [&](uint32_t i) {
+            // The two issuers take turns, one group of products (an item's first S; O and the next S)
+            // each: issued at the same time, the groups would interleave on the tensor pipe, both
+            // tiles would wait for both, and their softmaxes would run at the same time too.
+            uint32_t groups = 0;
+            const auto my_turn = [&] {
+                return wait_one(smem_u32(&tl->turn[t]), (groups++ & 1) ^ (t == 0 ? 1u : 0u), tmo, abort_flag, kWaitTurn);
+            };
+            const auto pass_turn = [&] { mbar_arrive(smem_u32(&tl->turn[t ^ 1])); };
+            const auto k_there = [&](uint32_t i) {
+                return wait_one(smem_u32(&tl->kfull[i % kStages]), (i / kStages) & 1, tmo, abort_flag, kWaitK);
+            };
+            const auto v_there = [&](uint32_t i) {
+                return wait_one(smem_u32(&tl->vfull[i % kStages]), (i / kStages) & 1, tmo, abort_flag, kWaitV);
+            };
+            const auto scores = [&](uint32_t i) {   // S of the CTA's unit i
                 const uint32_t st = i % kStages;
-                if (!wait_one(smem_u32(&tl->kfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitK)) return false;
-                tc_fence_after();
                 const uint64_t k0 = desc_k + st * (C::kTileBytes >> 4);   // descriptors count 16 bytes
 #pragma unroll
                 for (uint32_t k = 0; k < DP / 16; ++k) {
@@ -382,21 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                 tc_commit(smem_u32(&tl->sfull[t]));
                 mbar_arrive(smem_u32(&tl->sfull[t]));
                 tc_commit(smem_u32(&tl->kempty[st]));
-                return true;
             };
-            // (issuer) O += P V of unit i, once P is written and its V tile is there
-            const auto outputs = [&](uint32_t i, uint32_t block, bool add) {
+            const auto outputs = [&](uint32_t i, bool add) {   // O += P V of unit i
                 const uint32_t st = i % kStages;
-                if (!wait_one(smem_u32(&tl->pfull[t]), block & 1, tmo, abort_flag, kWaitP) ||
-                    !wait_one(smem_u32(&tl->vfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitV))
-                    return false;
-                tc_fence_after();
                 const uint64_t v0 = desc_v + st * (C::kTileBytes >> 4);
 #pragma unroll
                 for (uint32_t k = 0; k < kTile / 16; ++k)
                     tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
                 tc_commit(smem_u32(&tl->vempty[st]));
-                return true;
             };
             while (ok && u < u_end) {
                 const uint32_t j0 = static_cast<uint32_t>(u - it.first);
@@ -452,7 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     if (lane == 0) mbar_arrive(smem_u32(&tl->qfull[t]));
                     const uint32_t unit0 = static_cast<uint32_t>(u - u0);   // the CTA's units, those of both tiles
                     bool sent = true;
-                    if (issuer) sent = wait_one(smem_u32(&tl->qfull[t]), items & 1, tmo, abort_flag, kWaitQ) && scores(unit0);
+                    if (issuer) {
+                        sent = wait_one(smem_u32(&tl->qfull[t]), items & 1, tmo, abort_flag, kWaitQ) && k_there(unit0) && my_turn();
+                        if (sent) {
+                            tc_fence_after();
+                            scores(unit0);
+                            pass_turn();
+                        }
+                    }
                     ok = __all_sync(0xFFFFFFFFu, sent);
 
                     float ref = -INFINITY, l = 0.f;
@@ -503,12 +515,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&tl->pfull[t]));
                         if (issuer) {
-                            sent = outputs(unit0 + j, blocks, j > 0);
-                            // S of the next unit overwrites P, which O's products, ahead of it in order, have then read
-                            if (sent && j + 1 < cnt) sent = scores(unit0 + j + 1);
-                            if (j + 1 == cnt) {
-                                tc_commit(smem_u32(&tl->odone[t]));
-                                mbar_arrive(smem_u32(&tl->odone[t]));
+                            const uint32_t i = unit0 + j;
+                            const bool next = j + 1 < cnt;
+                            sent = wait_one(smem_u32(&tl->pfull[t]), blocks & 1, tmo, abort_flag, kWaitP) && v_there(i) &&
+                                   (!next || k_there(i + 1)) && my_turn();
+                            if (sent) {
+                                tc_fence_after();
+                                outputs(i, j > 0);
+                                if (next) {
+                                    // over P, which the products ahead in order have then read
+                                    scores(i + 1);
+                                } else {
+                                    tc_commit(smem_u32(&tl->odone[t]));
+                                    mbar_arrive(smem_u32(&tl->odone[t]));
+                                }
+                                pass_turn();
                             }
                         }
                         ok = __all_sync(0xFFFFFFFFu, sent);
@@ -558,13 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                                  max(static_cast<int>(j0 * kTile), edge_key(it.s, p.group, it.rb) / static_cast<int>(kTile) * static_cast<int>(kTile)),
                                  min(row_end, static_cast<int>((j0 + cnt) * kTile)), whole ? dst : nullptr, slot + t * kTile + row);
                 } else if (issuer) {
-                    // an item without this tile: its stages are released as they come
+                    // an item without this tile: its stages are released as they come, its turns passed on
+                    ok = my_turn();
+                    if (ok) pass_turn();
                     for (uint32_t j = 0; j < cnt && ok; ++j) {
-                        const uint32_t i = static_cast<uint32_t>(u - u0) + j, st = i % kStages;
-                        ok = wait_one(smem_u32(&tl->kfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitK);
-                        if (ok) mbar_arrive(smem_u32(&tl->kempty[st]));
-                        ok = ok && wait_one(smem_u32(&tl->vfull[st]), (i / kStages) & 1, tmo, abort_flag, kWaitV);
-                        if (ok) mbar_arrive(smem_u32(&tl->vempty[st]));
+                        const uint32_t i = static_cast<uint32_t>(u - u0) + j;
+                        ok = k_there(i);
+                        if (ok) mbar_arrive(smem_u32(&tl->kempty[i % kStages]));
+                        ok = ok && v_there(i);
+                        if (ok) mbar_arrive(smem_u32(&tl->vempty[i % kStages]));
+                        ok = ok && my_turn();
+                        if (ok) pass_turn();
                     }
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
