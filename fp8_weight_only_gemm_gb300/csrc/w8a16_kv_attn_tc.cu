@@ -7,19 +7,22 @@
 // over one CTA per SM in equal contiguous ranges; split items are joined through the
 // workspace by a second launch, in key order.
 //
-// A CTA. Warps 8-11 read a unit's E4M3 codes into registers a unit ahead, convert them to
+// A CTA. Warp 13 looks the units' pages and scales up, four units at a time, into a ring.
+// Warps 8-11 read a unit's E4M3 codes into registers a unit ahead, convert them to
 // FP16 (exact) and write the K and V tiles, [128 keys][DP] in 128-byte swizzled rows, two
 // stages each; the same layout serves K as a K-major operand and V, whose contraction
-// runs along its rows, as an MN-major one. Warps 0-3 and 4-7 own a row tile each; one
-// thread of each issues the tile's products, S = Q K^T (M = 128 rows, N = 128 keys) and
-// O += P V with P read from TMEM, so one tile's softmax runs under the other's products
-// (an issuing warp of its own would be a 13th, and leave 128 registers a thread instead of
-// 168). A thread owns a row, so no reduction crosses threads: a pass over its 128
-// scores in TMEM forms P (at most 2^15, FP16) in registers against the running maximum of the
-// units before; only where a row's maximum has risen by more than 2^8 is the maximum moved, O
-// rescaled and the pass repeated. P then overwrites the first columns of S.
+// runs along its rows, as an MN-major one. One thread of warp 12 issues the products, S = Q K^T
+// (M = 128 rows, N = 64 keys) and O += P V with P read from TMEM. Warps 0-3 and 4-7 own a
+// row tile each, a thread a row, so no reduction crosses threads. A unit's softmax goes in
+// two blocks of 64 keys, and O's products of the first run under the softmax of the second.
+// (S in N = 64 products, with a buffer each, would let a tile's softmax run on without a
+// pause, but they take 80 cycles for the 64 that N = 128 takes for twice the columns: the
+// A operand is read from shared memory again, and that is what these products wait for.)
+// A thread reads its 64 scores from TMEM, and only where their maximum exceeds the row's
+// running one by more than 8 is that moved and O rescaled; P (at most 2^15, FP16) overwrites
+// the first columns of S.
 //
-// TMEM: S/P of the tiles at columns 0 and 128, O at 256 and 256 + DP.
+// TMEM: S of tile t at columns 128 t, P of its blocks at 128 t and 128 t + 64, O at 256 + DP t.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -36,10 +39,12 @@ __device__ DeviceStatus g_kv_attn_tc_status;
 constexpr uint32_t kTile = 128;                // rows of a tile, and keys of a unit
 constexpr uint32_t kItemRows = 2 * kTile;
 constexpr uint32_t kSoftmaxWarps = 8, kConvWarps = 4;
-constexpr uint32_t kThreads = 32 * (kSoftmaxWarps + kConvWarps);
+constexpr uint32_t kIssueWarp = kSoftmaxWarps + kConvWarps, kLookWarp = kIssueWarp + 1;
+constexpr uint32_t kThreads = 32 * (kLookWarp + 1);
 constexpr uint32_t kWarpsAll = kThreads / 32;
+constexpr uint32_t kBlockKeys = 64;            // keys of a P
 constexpr uint32_t kStages = 2;
-constexpr uint32_t kScaleRing = 4;             // units whose page scales are held (see the converters)
+constexpr uint32_t kRing = 8, kLook = 4;        // units whose pages and scales are held, and looked up at a time
 constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
 constexpr uint32_t kChunk = 256;               // sequences whose unit counts are held at a time
 
@@ -49,18 +54,25 @@ struct Cfg {
     static constexpr uint32_t kHalfBytes = kTile * 128;             // a 64-column block of a tile
     static constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
     static constexpr uint32_t kTail = kV + kStages * kTileBytes;    // barriers, scales
-    static constexpr uint32_t kSmem = 1024 + kTail + 1024;
+    static constexpr uint32_t kSmem = 1024 + kTail + 2048;
+};
+struct Look {   // a unit, by its 8 groups of 16 keys
+    int64_t offset[8];                 // of the group's codes
+    float ks[8], lv[8], iv[8];         // K scale, log2 and reciprocal of the V scale
+    int last;                          // row of the last key there is
+    int edge;                          // some rows do not see all keys
 };
 struct Tail {
-    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2], odone[2], drain[2], turn[2];
+    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2][2], odone[2], drain;
+    uint64_t lfull[kRing], lempty[kRing];
     uint32_t tmem;
     int abort_flag;
     int nan_seen;
-    float ks[kScaleRing][8], lv[kScaleRing][8], iv[kScaleRing][8];   // per 16 keys of a unit
+    Look look[kRing];
 };
-static_assert(sizeof(Tail) <= 1024, "barrier block");
+static_assert(sizeof(Tail) <= 2048, "barrier block");
 
-enum Wait : unsigned { kWaitQ = 1, kWaitK, kWaitV, kWaitKFree, kWaitVFree, kWaitS, kWaitP, kWaitO, kWaitDrain, kWaitTurn };
+enum Wait : unsigned { kWaitQ = 1, kWaitK, kWaitV, kWaitKFree, kWaitVFree, kWaitS, kWaitP, kWaitO, kWaitDrain, kWaitLook, kWaitLookFree };
 
 // ------------------------------------------------------------ the schedule --
 // Keys that the last row of row block rb sees, and the units of its item.
@@ -235,10 +247,18 @@ __device__ __forceinline__ void convert16(const uint4& q, uint4& lo, uint4& hi) 
     e4m3x4_to_f16x4(q.z, hi.x, hi.y);
     e4m3x4_to_f16x4(q.w, hi.z, hi.w);
 }
-__device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& any) {
-    const uint32_t f = e4m3_nan_flags(w);
-    any |= f;
-    return w & ~((f >> 7) * 0xFFu);
+// NaN values (FP16) that this lane has stored to a V tile: 0 for the products, marked in the
+// outputs at the end (mark_nan). For units where some rows do not see all keys: there 0 * NaN
+// would reach them.
+__device__ __noinline__ void clean_tile(uint8_t* even, uint8_t* odd, uint32_t chunks, uint32_t halves, uint32_t half_bytes, Tail* tl) {
+    for (uint32_t i = 0; i < 2 * chunks; ++i) {
+        uint16_t* at = reinterpret_cast<uint16_t*>((i & 1 ? odd : even) + i / 2 % halves * half_bytes + i / 2 / halves * 1024);
+        for (int e = 0; e < 8; ++e)
+            if ((at[e] & 0x7FFF) > 0x7C00) {
+                at[e] = 0;
+                *static_cast<volatile int*>(&tl->nan_seen) = 1;
+            }
+    }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -253,30 +273,39 @@ __device__ __forceinline__ void mask_scores(uint32_t (&v)[32], int first, int en
     for (int e = 0; e < 32; ++e)
         if (first + e >= end) v[e] = 0xFF800000u;
 }
-// Their weights 2^(y - rc) as FP16 pairs, y = score ks rowf + log2(vs); the largest y
-// (ks rowf > 0: that of the largest score) and the sum of weight / vs are added to.
-__device__ __forceinline__ void score_weights(const uint32_t (&v)[32], const Tail* tl, uint32_t at, int ch, float rowf, float rc,
-                                              float& ymax, float& lsum, uint32_t (&pk)[16]) {
+// Their largest y = score ks rowf + log2(vs) (ks rowf > 0: that of the largest score);
+// ks, lv (and iv): of the two groups of 16 keys.
+__device__ __forceinline__ float score_max(const uint32_t (&v)[32], const float* ks, const float* lv, float rowf) {
+    float y = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) mx = max3(mx, __uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1]));
+        y = fmaxf(y, fmaf(mx, ks[g] * rowf, lv[g]));
+    }
+    return y;
+}
+// Their weights 2^(y - rc) as FP16 pairs; returns l + the sum of weight / vs.
+__device__ __forceinline__ float score_weights(const uint32_t (&v)[32], const float* ks, const float* lv, const float* iv, float rowf,
+                                               float rc, float l, uint32_t (&pk)[16]) {
     const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        const float f = tl->ks[at][2 * ch + g] * rowf, lv = tl->lv[at][2 * ch + g];
-        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(lv - rc, lv - rc);
+        const float f = ks[g] * rowf, d = lv[g] - rc;
+        const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(d, d);
         uint64_t s2 = pack_f32x2(0.f, 0.f);
-        float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-            const float x0 = __uint_as_float(v[16 * g + e]), x1 = __uint_as_float(v[16 * g + e + 1]);
-            mx = max3(mx, x0, x1);
-            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(x0, x1), ff, dd));
+            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1])), ff, dd));
             const float a = ex2(y.x), b = ex2(y.y);
             s2 = fma_f32x2(pack_f32x2(a, b), one, s2);
             pk[8 * g + e / 2] = pack2<true>(a, b);
         }
-        ymax = fmaxf(ymax, fmaf(mx, f, lv));
         const float2 s = unpack_f32x2(s2);
-        lsum = fmaf(s.x + s.y, tl->iv[at][2 * ch + g], lsum);
+        l = fmaf(s.x + s.y, iv[g], l);
     }
+    return l;
 }
 
 // NaN values of the keys [lo, hi), which the products at the causal edge left out, marked
@@ -309,20 +338,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     volatile int* const abort_flag = &tl->abort_flag;
     const uint64_t tmo = p.timeout_ns;
 
-    if (warp == kSoftmaxWarps) {
+    if (warp == kIssueWarp) {
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&tl->qfull[i]), 4);
                 mbar_init(smem_u32(&tl->kfull[i]), kConvWarps);
                 mbar_init(smem_u32(&tl->vfull[i]), kConvWarps);
-                mbar_init(smem_u32(&tl->kempty[i]), 2);   // both tiles' products
-                mbar_init(smem_u32(&tl->vempty[i]), 2);
+                mbar_init(smem_u32(&tl->kempty[i]), 1);
+                mbar_init(smem_u32(&tl->vempty[i]), 1);
                 mbar_init(smem_u32(&tl->sfull[i]), 2);   // the products' completion, and the issuer's own arrival
-                mbar_init(smem_u32(&tl->pfull[i]), 4);
+                for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&tl->pfull[i][k]), 4);
                 mbar_init(smem_u32(&tl->odone[i]), 2);
-                mbar_init(smem_u32(&tl->drain[i]), 1);
-                mbar_init(smem_u32(&tl->turn[i]), 1);
             }
+            for (uint32_t i = 0; i < kRing; ++i) {
+                mbar_init(smem_u32(&tl->lfull[i]), 1);
+                mbar_init(smem_u32(&tl->lempty[i]), 1);
+            }
+            mbar_init(smem_u32(&tl->drain), 1);
             tl->abort_flag = 0;
             tl->nan_seen = 0;
             fence_barrier_init();
@@ -363,46 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             const uint32_t t = warp / 4, row = (warp % 4) * 32 + lane;      // row of the tile
             const uint32_t lanes = ((warp % 4) * 32) << 16;
             const uint32_t tS = tm + t * kTile + lanes, tO = tm + 2 * kTile + t * DP + lanes;
-            const bool issuer = warp % 4 == 0 && lane == 0;
-            constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
-            uint32_t blocks = 0, items = 0;   // units and items of this tile
+            uint32_t blocks = 0;   // of this tile
             bool first_part = true, ok = true;
-            const uint64_t desc_q = smem_desc_kmajor_sw128(sbase + C::kQ + t * C::kTileBytes), desc_k = smem_desc_kmajor_sw128(sbase + C::kK),
-                           desc_v = smem_desc_mn_sw128(sbase + C::kV, C::kHalfBytes);
-            // The two issuers take turns, one group of products (an item's first S; O and the next S)
-            // each: issued at the same time, the groups would interleave on the tensor pipe, both
-            // tiles would wait for both, and their softmaxes would run at the same time too.
-            uint32_t groups = 0;
-            const auto my_turn = [&] {
-                return wait_one(smem_u32(&tl->turn[t]), (groups++ & 1) ^ (t == 0 ? 1u : 0u), tmo, abort_flag, kWaitTurn);
-            };
-            const auto pass_turn = [&] { mbar_arrive(smem_u32(&tl->turn[t ^ 1])); };
-            const auto k_there = [&](uint32_t i) {
-                return wait_one(smem_u32(&tl->kfull[i % kStages]), (i / kStages) & 1, tmo, abort_flag, kWaitK);
-            };
-            const auto v_there = [&](uint32_t i) {
-                return wait_one(smem_u32(&tl->vfull[i % kStages]), (i / kStages) & 1, tmo, abort_flag, kWaitV);
-            };
-            const auto scores = [&](uint32_t i) {   // S of the CTA's unit i
-                const uint32_t st = i % kStages;
-                const uint64_t k0 = desc_k + st * (C::kTileBytes >> 4);   // descriptors count 16 bytes
-#pragma unroll
-                for (uint32_t k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
-                    mma_ss(tm + t * kTile, desc_q + off, k0 + off, idS, k > 0);
-                }
-                tc_commit(smem_u32(&tl->sfull[t]));
-                mbar_arrive(smem_u32(&tl->sfull[t]));
-                tc_commit(smem_u32(&tl->kempty[st]));
-            };
-            const auto outputs = [&](uint32_t i, bool add) {   // O += P V of unit i
-                const uint32_t st = i % kStages;
-                const uint64_t v0 = desc_v + st * (C::kTileBytes >> 4);
-#pragma unroll
-                for (uint32_t k = 0; k < kTile / 16; ++k)
-                    tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
-                tc_commit(smem_u32(&tl->vempty[st]));
-            };
             while (ok && u < u_end) {
                 const uint32_t j0 = static_cast<uint32_t>(u - it.first);
                 const uint32_t cnt = static_cast<uint32_t>(min(static_cast<uint64_t>(it.n - j0), u_end - u));
@@ -456,48 +450,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&tl->qfull[t]));
                     const uint32_t unit0 = static_cast<uint32_t>(u - u0);   // the CTA's units, those of both tiles
-                    bool sent = true;
-                    if (issuer) {
-                        sent = wait_one(smem_u32(&tl->qfull[t]), items & 1, tmo, abort_flag, kWaitQ) && k_there(unit0) && my_turn();
-                        if (sent) {
-                            tc_fence_after();
-                            scores(unit0);
-                            pass_turn();
-                        }
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, sent);
 
                     float ref = -INFINITY, l = 0.f;
-                    for (uint32_t j = 0; j < cnt && ok; ++j, ++blocks) {
-                        if (!(ok = wait_warp(smem_u32(&tl->sfull[t]), blocks & 1, tmo, abort_flag, kWaitS))) break;
-                        tc_fence_after();
-                        const uint32_t at = (unit0 + j) % kScaleRing;
-                        const int key0 = static_cast<int>((j0 + j) * kTile);
-                        const bool edge = key0 + static_cast<int>(kTile) > warp_min;
-                        // ---- P against the maximum of the units before; again, where the unit's own is far above it
-                        const int end = edge ? row_end - key0 : static_cast<int>(kTile);
-                        uint32_t pk[4][16];
-                        float lsum;
 #pragma unroll 1
-                        for (int pass = 0; pass < 2; ++pass) {
-                            const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
-                            float ymax = -INFINITY;
-                            lsum = 0.f;
-                            uint32_t v[2][32];
-                            tmem_ld32(tS, v[0]);
-#pragma unroll
-                            for (int ch = 0; ch < 4; ++ch) {
-                                tc_wait_ld();
-                                if (ch < 3) tmem_ld32(tS + 32 * (ch + 1), v[(ch + 1) & 1]);
-                                if (edge) mask_scores(v[ch & 1], 32 * ch, end);
-                                score_weights(v[ch & 1], tl, at, ch, rowf, rc, ymax, lsum, pk[ch]);
-                            }
-                            if (!__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) break;
+                    for (uint32_t j = 0; j < 2 * cnt; ++j, ++blocks) {
+                        const uint32_t half = j & 1, tB = tS + half * kBlockKeys;
+                        if (half == 0) {
+                            if (!(ok = wait_warp(smem_u32(&tl->sfull[t]), (blocks >> 1) & 1, tmo, abort_flag, kWaitS))) break;
+                            tc_fence_after();
+                        }
+                        const Look& look = tl->look[(unit0 + j / 2) % kRing];
+                        const int key0 = static_cast<int>(j0 * kTile + j * kBlockKeys);
+                        // ---- the row's 64 scores, and the largest y = score ks rowf + log2(vs)
+                        uint32_t v[2][32];
+                        tmem_ld32(tB, v[0]);
+                        tmem_ld32(tB + 32, v[1]);
+                        tc_wait_ld();
+                        if (key0 + static_cast<int>(kBlockKeys) > warp_min) {
+                            mask_scores(v[0], 0, row_end - key0);
+                            mask_scores(v[1], 32, row_end - key0);
+                        }
+                        const float *ks = look.ks + 4 * half, *lv = look.lv + 4 * half, *iv = look.iv + 4 * half;
+                        const float ymax = fmaxf(score_max(v[0], ks, lv, rowf), score_max(v[1], ks + 2, lv + 2, rowf));
+                        if (__any_sync(0xFFFFFFFFu, ymax > ref + kRise)) {
+                            // the maximum moves: the sum and, once the products so far are in it, O are rescaled
                             const float m_new = fmaxf(ref, ymax);
                             const float a = ref == -INFINITY ? 0.f : ex2(ref - m_new);
                             l *= a;
                             ref = m_new;
                             if (j > 0) {
+                                if (!(ok = wait_warp(smem_u32(&tl->odone[t]), (blocks - 1) & 1, tmo, abort_flag, kWaitO))) break;
+                                tc_fence_after();
 #pragma unroll 1
                                 for (uint32_t d = 0; d < DP; d += 8) {
                                     float o[8];
@@ -507,35 +490,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                                 }
                             }
                         }
-                        l += lsum;
+                        const float rc = ref == -INFINITY ? 0.f : ref - kPBits;
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) tmem_st_32x32b_x16(tS + 16 * ch, pk[ch]);
+                        for (int ch = 0; ch < 2; ++ch) {
+                            uint32_t pk[16];
+                            l = score_weights(v[ch], ks + 2 * ch, lv + 2 * ch, iv + 2 * ch, rowf, rc, l, pk);
+                            tmem_st_32x32b_x16(tB + 16 * ch, pk);
+                        }
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&tl->pfull[t]));
-                        if (issuer) {
-                            const uint32_t i = unit0 + j;
-                            const bool next = j + 1 < cnt;
-                            sent = wait_one(smem_u32(&tl->pfull[t]), blocks & 1, tmo, abort_flag, kWaitP) && v_there(i) &&
-                                   (!next || k_there(i + 1)) && my_turn();
-                            if (sent) {
-                                tc_fence_after();
-                                outputs(i, j > 0);
-                                if (next) {
-                                    // over P, which the products ahead in order have then read
-                                    scores(i + 1);
-                                } else {
-                                    tc_commit(smem_u32(&tl->odone[t]));
-                                    mbar_arrive(smem_u32(&tl->odone[t]));
-                                }
-                                pass_turn();
-                            }
-                        }
-                        ok = __all_sync(0xFFFFFFFFu, sent);
+                        if (lane == 0) mbar_arrive(smem_u32(&tl->pfull[t][half]));
                     }
-                    if (!ok || !(ok = wait_warp(smem_u32(&tl->odone[t]), items & 1, tmo, abort_flag, kWaitO))) break;
-                    ++items;
+                    // odone completes once a block. The last S has shown the block two before it done; a
+                    // parity tells one phase from the next only, so the last two are waited for in turn.
+                    ok = ok && wait_warp(smem_u32(&tl->odone[t]), blocks & 1, tmo, abort_flag, kWaitO) &&
+                         wait_warp(smem_u32(&tl->odone[t]), (blocks - 1) & 1, tmo, abort_flag, kWaitO);
+                    if (!ok) break;
                     tc_fence_after();
                     // ---- outputs, or this range's part of them ([d][row], coalesced over rows)
                     const bool whole = cnt == it.n;
@@ -578,29 +549,144 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         mark_nan(p, it.b, it.h,
                                  max(static_cast<int>(j0 * kTile), edge_key(it.s, p.group, it.rb) / static_cast<int>(kTile) * static_cast<int>(kTile)),
                                  min(row_end, static_cast<int>((j0 + cnt) * kTile)), whole ? dst : nullptr, slot + t * kTile + row);
-                } else if (issuer) {
-                    // an item without this tile: its stages are released as they come, its turns passed on
-                    ok = my_turn();
-                    if (ok) pass_turn();
-                    for (uint32_t j = 0; j < cnt && ok; ++j) {
-                        const uint32_t i = static_cast<uint32_t>(u - u0) + j;
-                        ok = k_there(i);
-                        if (ok) mbar_arrive(smem_u32(&tl->kempty[i % kStages]));
-                        ok = ok && v_there(i);
-                        if (ok) mbar_arrive(smem_u32(&tl->vempty[i % kStages]));
-                        ok = ok && my_turn();
-                        if (ok) pass_turn();
-                    }
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok);
                 first_part = false;
                 u += cnt;
                 if (u < u_end) next_item(p, it);
             }
-            if (issuer) {   // every product issued ends before TMEM is released
-                tc_commit(smem_u32(&tl->drain[t]));
+        } else if (warp == kIssueWarp) {
+            // ------------------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
+                constexpr uint32_t kBlockDesc = (kBlockKeys * 128) >> 4;   // descriptors count 16 bytes
+                const uint64_t desc_q = smem_desc_kmajor_sw128(sbase + C::kQ), desc_k = smem_desc_kmajor_sw128(sbase + C::kK),
+                               desc_v = smem_desc_mn_sw128(sbase + C::kV, C::kHalfBytes);
+                const auto scores = [&](uint32_t t, uint32_t unit) {   // S of the CTA's unit
+                    const uint64_t q0 = desc_q + t * (C::kTileBytes >> 4), k0 = desc_k + unit % kStages * (C::kTileBytes >> 4);
+#pragma unroll
+                    for (uint32_t k = 0; k < DP / 16; ++k) {
+                        const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
+                        mma_ss(tm + t * kTile, q0 + off, k0 + off, idS, k > 0);
+                    }
+                    tc_commit(smem_u32(&tl->sfull[t]));
+                    mbar_arrive(smem_u32(&tl->sfull[t]));
+                };
+                const auto outputs = [&](uint32_t t, uint32_t i, bool add) {   // O += P V of its block i (64 keys)
+                    const uint64_t v0 = desc_v + i / 2 % kStages * (C::kTileBytes >> 4) + i % 2 * kBlockDesc;
+#pragma unroll
+                    for (uint32_t k = 0; k < kBlockKeys / 16; ++k)
+                        tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + i % 2 * kBlockKeys + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
+                    tc_commit(smem_u32(&tl->odone[t]));
+                    mbar_arrive(smem_u32(&tl->odone[t]));
+                };
+                const auto k_there = [&](uint32_t unit) {
+                    return wait_one(smem_u32(&tl->kfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitK);
+                };
+                bool ok = true;
+                uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // items and blocks of a tile so far
+                while (ok && u < u_end) {
+                    const uint32_t cnt = static_cast<uint32_t>(min(it.first + it.n - u, u_end - u));
+                    const uint32_t tiles = static_cast<uint32_t>(it.s.count) * p.group > it.rb * kItemRows + kTile ? 2 : 1;
+                    const uint32_t unit0 = static_cast<uint32_t>(u - u0);
+                    ok = k_there(unit0);
+                    for (uint32_t t = 0; t < tiles && ok; ++t) {
+                        ok = wait_one(smem_u32(&tl->qfull[t]), nq[t]++ & 1, tmo, abort_flag, kWaitQ);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(t, unit0);
+                    }
+                    if (ok) tc_commit(smem_u32(&tl->kempty[unit0 % kStages]));
+#pragma unroll 1
+                    for (uint32_t j = 0; j < 2 * cnt && ok; ++j) {
+                        const uint32_t i = 2 * unit0 + j, unit = i / 2;
+                        const bool next = i % 2 == 1 && j + 1 < 2 * cnt;   // a unit follows this block
+                        if (i % 2 == 0)
+                            ok = wait_one(smem_u32(&tl->vfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitV);
+                        else if (next)
+                            ok = k_there(unit + 1);
+                        for (uint32_t t = 0; t < tiles && ok; ++t) {
+                            ok = wait_one(smem_u32(&tl->pfull[t][i % 2]), (np[t]++ >> 1) & 1, tmo, abort_flag, kWaitP);
+                            if (!ok) break;
+                            tc_fence_after();
+                            outputs(t, i, j > 0);
+                            if (next) scores(t, unit + 1);   // over P, which the products ahead in order have then read
+                        }
+                        if (i % 2 == 1) {   // the unit's V, and what was looked up for it, are done with
+                            tc_commit(smem_u32(&tl->vempty[unit % kStages]));
+                            tc_commit(smem_u32(&tl->lempty[unit % kRing]));
+                        }
+                        if (next) tc_commit(smem_u32(&tl->kempty[(unit + 1) % kStages]));
+                    }
+                    u += cnt;
+                    if (u < u_end) next_item(p, it);
+                }
+                // every product issued ends before TMEM is released
+                tc_commit(smem_u32(&tl->drain));
                 volatile int never = 0;
-                mbar_wait(smem_u32(&tl->drain[t]), 0, globaltimer_ns() + tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
+                mbar_wait(smem_u32(&tl->drain), 0, globaltimer_ns() + tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
+            }
+        } else if (warp == kLookWarp) {
+            // ------------------------------------------------- pages and scales
+            // lane 8 q + g: group g of the q-th of the next kLook units
+            const uint32_t q = lane / 8, g = lane % 8;
+            int it_end = block_end(it.s, p.group, it.rb), it_edge = edge_key(it.s, p.group, it.rb);
+            uint32_t i = 0;   // the CTA's units so far
+            bool ok = true;
+#pragma unroll 1
+            while (ok && u < u_end) {
+                const uint32_t n = static_cast<uint32_t>(min(static_cast<uint64_t>(kLook), u_end - u));
+                int key0 = 0, end = 0, edge = 0;
+                uint32_t b = 0, h = 0;
+#pragma unroll 1
+                for (uint32_t k = 0; k < n; ++k, ++u) {
+                    if (u >= it.first + it.n) {
+                        next_item(p, it);
+                        it_end = block_end(it.s, p.group, it.rb);
+                        it_edge = edge_key(it.s, p.group, it.rb);
+                    }
+                    if (k == q) {
+                        key0 = static_cast<int>(u - it.first) * static_cast<int>(kTile);
+                        end = it_end;
+                        edge = it.s.count > 1 && key0 + static_cast<int>(kTile) > it_edge;
+                        b = it.b;
+                        h = it.h;
+                    }
+                }
+                const int key = key0 + 16 * static_cast<int>(g);
+                int page = -1;
+                if (q < n && key < end) {
+                    page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
+                    if (static_cast<uint32_t>(page) >= p.c.num_pages) {
+                        record_failure(&g_kv_attn_tc_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(page));
+                        page = -1;
+                    }
+                }
+                float sk = 1.f, sv = 1.f;
+                if (page >= 0) {
+                    const int64_t at = static_cast<int64_t>(page) * p.c.scale_page_stride + static_cast<int64_t>(h) * p.c.scale_head_stride;
+                    sk = p.c.k_scale[at];
+                    sv = p.c.v_scale[at];
+                    if (sk < kMinScale) sk = kMinScale;
+                    if (sv < kMinScale) sv = kMinScale;
+                }
+                for (uint32_t k = 0; k < n && ok; ++k)
+                    ok = wait_warp(smem_u32(&tl->lempty[(i + k) % kRing]), (((i + k) / kRing) & 1) ^ 1, tmo, abort_flag, kWaitLookFree);
+                if (!ok) break;
+                if (q < n) {
+                    Look& look = tl->look[(i + q) % kRing];
+                    look.offset[g] = static_cast<int64_t>(max(page, 0)) * p.c.page_stride + static_cast<int64_t>(h) * p.c.head_stride +
+                                     static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
+                    look.ks[g] = sk;
+                    look.lv[g] = __log2f(sv);
+                    look.iv[g] = __frcp_rn(sv);
+                    if (g == 0) {
+                        look.last = max(end - 1 - key0, 0);
+                        look.edge = edge;
+                    }
+                }
+                __syncwarp();
+                if (lane < n) mbar_arrive(smem_u32(&tl->lfull[(i + lane) % kRing]));
+                i += n;
             }
         } else {
             // --------------------------------------------- codes -> FP16 tiles
@@ -611,133 +697,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             const uint32_t cw = warp - kSoftmaxWarps, lrow = lane & 7, lch = lane >> 3;
             const uint32_t off0 = min(16 * lch, p.c.head_dim - 16), off1 = min(64 + 16 * lch, p.c.head_dim - 16);
             const uint32_t st0 = (cw * 32 + lrow) * 128 + (((2 * lch) ^ lrow) << 4), st1 = (cw * 32 + lrow) * 128 + (((2 * lch + 1) ^ lrow) << 4);
-            struct Unit {
-                int key0, end;
-                bool edge;
-                uint32_t b, h;
-            };
-            uint64_t un = u0;   // next unit to look up
-            int it_end = block_end(it.s, p.group, it.rb), it_edge = edge_key(it.s, p.group, it.rb);
-            const auto next_unit = [&](Unit& x) {
-                if (un >= u_end) return false;
-                if (un >= it.first + it.n) {
-                    next_item(p, it);
-                    it_end = block_end(it.s, p.group, it.rb);
-                    it_edge = edge_key(it.s, p.group, it.rb);
-                }
-                x.key0 = static_cast<int>(un - it.first) * static_cast<int>(kTile);
-                x.end = it_end;
-                x.edge = it.s.count > 1 && x.key0 + static_cast<int>(kTile) > it_edge;
-                x.b = it.b;
-                x.h = it.h;
-                ++un;
-                return true;
-            };
-            // lane l < 8: page and scales of keys [16 l, 16 l + 16) of a unit
-            int page = -1;
-            float mk = 1.f, mv = 1.f;
-            const auto load_meta = [&](const Unit& x) {
-                page = -1;
-                mk = mv = 1.f;
-                const int key = x.key0 + 16 * static_cast<int>(lane);
-                if (lane < 8 && key < x.end) {
-                    const int pg = p.b.page_table[static_cast<int64_t>(x.b) * p.b.page_table_stride + (key >> p.page_shift)];
-                    if (pg < 0 || pg >= static_cast<int>(p.c.num_pages)) {
-                        record_failure(&g_kv_attn_tc_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pg));
-                    } else {
-                        const int64_t s = static_cast<int64_t>(pg) * p.c.scale_page_stride + static_cast<int64_t>(x.h) * p.c.scale_head_stride;
-                        page = pg;
-                        mk = p.c.k_scale[s];
-                        mv = p.c.v_scale[s];
-                        if (mk < kMinScale) mk = kMinScale;
-                        if (mv < kMinScale) mv = kMinScale;
-                    }
-                }
-            };
+            const uint32_t units = static_cast<uint32_t>(u_end - u0);
             // Rows past the last key, and chunks past the head, repeat the last ones: their scores are
             // masked and their queries and outputs are not there, and their values are as finite as
-            // those that they repeat (in a unit where rows see different keys: after drop_nan).
-            const auto load_codes = [&](const Unit& x, const void* codes, uint4 (&q)[CH]) {
-                const uint8_t* row[4];   // this lane's rows of 8
-                const int last = max(x.end - 1 - x.key0, 0);
+            // those that they repeat (in a unit where rows see different keys: after clean_tile).
+            int64_t row[4];   // this lane's rows of 8 of the unit being loaded
+            const auto load_codes = [&](const void* codes, uint4 (&c)[CH]) {
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    const int r = min(static_cast<int>(32 * cw + 8 * i + lrow), last);
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r >> 4);
-                    row[i] = static_cast<const uint8_t*>(codes) + static_cast<int64_t>(max(pg, 0)) * p.c.page_stride +
-                             static_cast<int64_t>(x.h) * p.c.head_stride +
-                             static_cast<int64_t>((x.key0 + r) & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
-                }
-#pragma unroll
-                for (uint32_t i = 0; i < CH; ++i)
-                    q[i] = *reinterpret_cast<const uint4*>(row[i / kHalves] + (i % kHalves ? off1 : off0));
+                for (uint32_t i = 0; i < CH; ++i)   // L2 only: the few KB of L1 beside the tiles are for what is used again
+                    c[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + row[i / kHalves] + (i % kHalves ? off1 : off0)));
             };
-            const auto store_tile = [&](uint32_t tile, uint4 (&q)[CH], bool clean) {
-                if (clean) {   // NaN values at the causal edge: 0 here, marked at the end (mark_nan)
-                    uint32_t any = 0;
-#pragma unroll
-                    for (uint32_t i = 0; i < CH; ++i) {
-                        q[i].x = drop_nan(q[i].x, any);
-                        q[i].y = drop_nan(q[i].y, any);
-                        q[i].z = drop_nan(q[i].z, any);
-                        q[i].w = drop_nan(q[i].w, any);
-                    }
-                    if (any) *static_cast<volatile int*>(&tl->nan_seen) = 1;
-                }
+            const auto store_tile = [&](uint32_t tile, const uint4 (&c)[CH]) {
 #pragma unroll
                 for (uint32_t i = 0; i < CH; ++i) {
                     uint4 lo, hi;
-                    convert16(q[i], lo, hi);
+                    convert16(c[i], lo, hi);
                     uint8_t* at = smem + tile + (i % kHalves) * C::kHalfBytes + i / kHalves * 1024;
                     *reinterpret_cast<uint4*>(at + st0) = lo;
                     *reinterpret_cast<uint4*>(at + st1) = hi;
                 }
+            };
+            const auto signal = [&](uint64_t* bar) {
                 fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(bar));
             };
-            // step i: store unit i (its codes in registers), load unit i + 1's, look unit i + 2's pages up
-            Unit cur{}, ahead{};
+            // step i: store unit i (codes in registers), load unit i + 1's
             uint4 kq[CH], vq[CH];
-            float sk = 1.f, sv = 1.f;
-            bool have = false, more = next_unit(ahead);
-            load_meta(ahead);
+            int edge = 0, next_edge = 0;
 #pragma unroll 1
-            for (uint32_t i = 0xFFFFFFFFu; have || more; ++i) {
+            for (uint32_t i = 0xFFFFFFFFu; i + 1 <= units; ++i) {
                 const uint32_t st = i % kStages, parity = ((i / kStages) & 1) ^ 1;
+                const bool have = i != 0xFFFFFFFFu, more = i + 1 < units;
                 if (have) {
                     if (!wait_warp(smem_u32(&tl->kempty[st]), parity, tmo, abort_flag, kWaitKFree)) break;
-                    store_tile(C::kK + st * C::kTileBytes, kq, false);
-                    // Slot i % 4 is free: unit i - 4 was read before unit i - 2's products could free this K stage
-                    if (warp == kSoftmaxWarps && lane < 8) {
-                        tl->ks[i % kScaleRing][lane] = sk;
-                        tl->lv[i % kScaleRing][lane] = __log2f(sv);
-                        tl->iv[i % kScaleRing][lane] = __frcp_rn(sv);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&tl->kfull[st]));
+                    store_tile(C::kK + st * C::kTileBytes, kq);
+                    signal(&tl->kfull[st]);
                 }
-                if (more) load_codes(ahead, p.c.k_codes, kq);
+                if (more) {
+                    if (!wait_warp(smem_u32(&tl->lfull[(i + 1) % kRing]), ((i + 1) / kRing) & 1, tmo, abort_flag, kWaitLook)) break;
+                    const Look& look = tl->look[(i + 1) % kRing];
+                    const int last = look.last;
+                    next_edge = look.edge;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) {
+                        const int r = min(static_cast<int>(32 * cw + 8 * k + lrow), last);
+                        row[k] = look.offset[r >> 4] + static_cast<int64_t>(r & 15) * p.c.token_stride;
+                    }
+                    load_codes(p.c.k_codes, kq);
+                }
                 if (have) {
                     if (!wait_warp(smem_u32(&tl->vempty[st]), parity, tmo, abort_flag, kWaitVFree)) break;
-                    store_tile(C::kV + st * C::kTileBytes, vq, cur.edge);
-                    if (lane == 0) mbar_arrive(smem_u32(&tl->vfull[st]));
+                    store_tile(C::kV + st * C::kTileBytes, vq);
+                    if (edge) clean_tile(smem + C::kV + st * C::kTileBytes + st0, smem + C::kV + st * C::kTileBytes + st1, CH, kHalves, C::kHalfBytes, tl);
+                    signal(&tl->vfull[st]);
                 }
-                have = more;
-                if (more) {
-                    load_codes(ahead, p.c.v_codes, vq);
-                    cur = ahead;
-                    sk = mk;
-                    sv = mv;
-                    more = next_unit(ahead);
-                    if (more) load_meta(ahead);
-                }
+                if (more) load_codes(p.c.v_codes, vq);
+                edge = next_edge;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSoftmaxWarps) tmem_dealloc(tm, 512);
+    if (warp == kIssueWarp) tmem_dealloc(tm, 512);
 }
 
 // Joins the parts of split items in key order. blockIdx.x = c - 1 for the boundary before
