@@ -261,6 +261,11 @@ __device__ __noinline__ void clean_tile(uint8_t* even, uint8_t* odd, uint32_t ch
     }
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Tail* const tl = reinterpret_cast<Tail*>(smem + C::kTail);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     volatile int* const abort_flag = &tl->abort_flag;
     const uint64_t tmo = p.timeout_ns;
 
@@ -556,71 +561,90 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             }
         } else if (warp == kIssueWarp) {
             // ------------------------------------------------------- products
-            if (lane == 0) {
-                constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
-                constexpr uint32_t kBlockDesc = (kBlockKeys * 128) >> 4;   // descriptors count 16 bytes
-                const uint64_t desc_q = smem_desc_kmajor_sw128(sbase + C::kQ), desc_k = smem_desc_kmajor_sw128(sbase + C::kK),
-                               desc_v = smem_desc_mn_sw128(sbase + C::kV, C::kHalfBytes);
-                const auto scores = [&](uint32_t t, uint32_t unit) {   // S of the CTA's unit
-                    const uint64_t q0 = desc_q + t * (C::kTileBytes >> 4), k0 = desc_k + unit % kStages * (C::kTileBytes >> 4);
+            // The whole warp goes through the loops, on broadcast counts, and one elected lane issues:
+            // so descriptors are formed in uniform registers. (A lane of its own formed them in
+            // ordinary ones and took longer over each product than the tensor core.)
+            constexpr uint32_t idS = idesc_f16(kTile, kTile, false), idO = idesc_f16(kTile, DP, true);
+            constexpr uint32_t kBlockDesc = (kBlockKeys * 128) >> 4;   // descriptors count 16 bytes
+            const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
+            const uint64_t desc_q = smem_desc_kmajor_sw128(sb + C::kQ), desc_k = smem_desc_kmajor_sw128(sb + C::kK),
+                           desc_v = smem_desc_mn_sw128(sb + C::kV, C::kHalfBytes);
+            const bool elected = elect_one();
+            const auto scores = [&](uint32_t t, uint32_t unit) {   // S of the CTA's unit
+                const uint64_t q0 = desc_q + t * (C::kTileBytes >> 4), k0 = desc_k + unit % kStages * (C::kTileBytes >> 4);
+                if (elected) {
 #pragma unroll
                     for (uint32_t k = 0; k < DP / 16; ++k) {
                         const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_ss(tm + t * kTile, q0 + off, k0 + off, idS, k > 0);
+                        mma_ss(tmu + t * kTile, q0 + off, k0 + off, idS, k > 0);
                     }
                     tc_commit(smem_u32(&tl->sfull[t]));
                     mbar_arrive(smem_u32(&tl->sfull[t]));
-                };
-                const auto outputs = [&](uint32_t t, uint32_t i, bool add) {   // O += P V of its block i (64 keys)
-                    const uint64_t v0 = desc_v + i / 2 % kStages * (C::kTileBytes >> 4) + i % 2 * kBlockDesc;
+                }
+            };
+            const auto outputs = [&](uint32_t t, uint32_t unit, uint32_t half, bool add) {   // O += P V of half a unit
+                const uint64_t v0 = desc_v + unit % kStages * (C::kTileBytes >> 4) + half * kBlockDesc;
+                if (elected) {
 #pragma unroll
                     for (uint32_t k = 0; k < kBlockKeys / 16; ++k)
-                        tc_mma_a_tmem(tm + 2 * kTile + t * DP, tm + t * kTile + i % 2 * kBlockKeys + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
+                        tc_mma_a_tmem(tmu + 2 * kTile + t * DP, tmu + t * kTile + half * kBlockKeys + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
                     tc_commit(smem_u32(&tl->odone[t]));
                     mbar_arrive(smem_u32(&tl->odone[t]));
-                };
-                const auto k_there = [&](uint32_t unit) {
-                    return wait_one(smem_u32(&tl->kfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitK);
-                };
-                bool ok = true;
-                uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // items and blocks of a tile so far
-                while (ok && u < u_end) {
-                    const uint32_t cnt = static_cast<uint32_t>(min(it.first + it.n - u, u_end - u));
-                    const uint32_t tiles = static_cast<uint32_t>(it.s.count) * p.group > it.rb * kItemRows + kTile ? 2 : 1;
-                    const uint32_t unit0 = static_cast<uint32_t>(u - u0);
-                    ok = k_there(unit0);
-                    for (uint32_t t = 0; t < tiles && ok; ++t) {
-                        ok = wait_one(smem_u32(&tl->qfull[t]), nq[t]++ & 1, tmo, abort_flag, kWaitQ);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(t, unit0);
-                    }
-                    if (ok) tc_commit(smem_u32(&tl->kempty[unit0 % kStages]));
+                }
+            };
+            bool ok = true;
+            uint32_t unit = 0;                            // the CTA's units so far
+            uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // items and units of each tile so far
+            while (ok && u < u_end) {
+                const uint32_t cnt = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(it.first + it.n - u, u_end - u)), 0);
+                const uint32_t tiles = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(it.s.count) * p.group > it.rb * kItemRows + kTile ? 2u : 1u, 0);
+                ok = wait_warp(smem_u32(&tl->kfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitK) &&
+                     wait_warp(smem_u32(&tl->qfull[0]), nq0++ & 1, tmo, abort_flag, kWaitQ) &&
+                     (tiles == 1 || wait_warp(smem_u32(&tl->qfull[1]), nq1++ & 1, tmo, abort_flag, kWaitQ));
+                if (!ok) break;
+                tc_fence_after();
+                scores(0, unit);
+                if (tiles == 2) scores(1, unit);
+                if (elected) tc_commit(smem_u32(&tl->kempty[unit % kStages]));
 #pragma unroll 1
-                    for (uint32_t j = 0; j < 2 * cnt && ok; ++j) {
-                        const uint32_t i = 2 * unit0 + j, unit = i / 2;
-                        const bool next = i % 2 == 1 && j + 1 < 2 * cnt;   // a unit follows this block
-                        if (i % 2 == 0)
-                            ok = wait_one(smem_u32(&tl->vfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitV);
-                        else if (next)
-                            ok = k_there(unit + 1);
-                        for (uint32_t t = 0; t < tiles && ok; ++t) {
-                            ok = wait_one(smem_u32(&tl->pfull[t][i % 2]), (np[t]++ >> 1) & 1, tmo, abort_flag, kWaitP);
-                            if (!ok) break;
-                            tc_fence_after();
-                            outputs(t, i, j > 0);
-                            if (next) scores(t, unit + 1);   // over P, which the products ahead in order have then read
-                        }
-                        if (i % 2 == 1) {   // the unit's V, and what was looked up for it, are done with
-                            tc_commit(smem_u32(&tl->vempty[unit % kStages]));
-                            tc_commit(smem_u32(&tl->lempty[unit % kRing]));
-                        }
+                for (uint32_t j = 0; j < cnt; ++j, ++unit) {
+                    // the first half's products of both tiles
+                    ok = wait_warp(smem_u32(&tl->vfull[unit % kStages]), (unit / kStages) & 1, tmo, abort_flag, kWaitV) &&
+                         wait_warp(smem_u32(&tl->pfull[0][0]), np0 & 1, tmo, abort_flag, kWaitP);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outputs(0, unit, 0, j > 0);
+                    if (tiles == 2) {
+                        if (!(ok = wait_warp(smem_u32(&tl->pfull[1][0]), np1 & 1, tmo, abort_flag, kWaitP))) break;
+                        tc_fence_after();
+                        outputs(1, unit, 0, j > 0);
+                    }
+                    // the second half's, each followed by the next unit's S over P, which the products
+                    // ahead of it in order have then read
+                    const bool next = j + 1 < cnt;
+                    ok = (!next || wait_warp(smem_u32(&tl->kfull[(unit + 1) % kStages]), ((unit + 1) / kStages) & 1, tmo, abort_flag, kWaitK)) &&
+                         wait_warp(smem_u32(&tl->pfull[0][1]), np0++ & 1, tmo, abort_flag, kWaitP);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outputs(0, unit, 1, true);
+                    if (next) scores(0, unit + 1);
+                    if (tiles == 2) {
+                        if (!(ok = wait_warp(smem_u32(&tl->pfull[1][1]), np1++ & 1, tmo, abort_flag, kWaitP))) break;
+                        tc_fence_after();
+                        outputs(1, unit, 1, true);
+                        if (next) scores(1, unit + 1);
+                    }
+                    if (elected) {   // the unit's V, and what was looked up for it, are done with
+                        tc_commit(smem_u32(&tl->vempty[unit % kStages]));
+                        tc_commit(smem_u32(&tl->lempty[unit % kRing]));
                         if (next) tc_commit(smem_u32(&tl->kempty[(unit + 1) % kStages]));
                     }
-                    u += cnt;
-                    if (u < u_end) next_item(p, it);
                 }
-                // every product issued ends before TMEM is released
+                u += cnt;
+                if (ok && u < u_end) next_item(p, it);
+            }
+            // every product issued ends before TMEM is released
+            if (elected) {
                 tc_commit(smem_u32(&tl->drain));
                 volatile int never = 0;
                 mbar_wait(smem_u32(&tl->drain), 0, globaltimer_ns() + tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
