@@ -49,6 +49,8 @@ int check_cache(const char* who, const w8a16_kv_cache_t* c) {
         return api_fail(W8A16_ERR_ALIGN, w + ": cache codes need 16-byte alignment, scales 4");
     if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
         return api_fail(W8A16_ERR_ALIGN, w + ": cache strides must be multiples of 16 bytes");
+    if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->token_stride > 1 << 22)
+        return api_fail(W8A16_ERR_RANGE, w + ": cache strides must not be negative, token_stride at most 2^22 bytes");
     return W8A16_OK;
 }
 

@@ -5,10 +5,11 @@
 // with E4M3 codes k_j, V_j and the page scales ks_j, vs_j. One pass keeps a running
 // maximum m of y_j = log2(e) c ks_j (q . k_j) + log2(vs_j), the sum l and the
 // unnormalised output in FP32:
-//     P_j = 2^(y_j - m + 15),   O += P_j V_j,   l += P_j / vs_j.
-// The value scale is part of the maximum, so P_j <= 2^15 whatever the scales are, and
-// P is rounded once, to FP16: 11 bits, with 2^-39 of the largest weight still
-// representable. Both products run on FP16 operands: E4M3 converts to FP16 exactly
+//     P_j = 2^(y_j - m + 7),   O += P_j V_j,   l += P_j / vs_j.
+// m moves only when a y exceeds it by more than 8 (few steps do after the first; moving it
+// means rescaling O). The value scale is part of the maximum, so P_j <= 2^15 whatever the
+// scales are, and P is rounded once, to FP16: 11 bits, with 2^-31 of the largest weight
+// still representable. Both products run on FP16 operands: E4M3 converts to FP16 exactly
 // (one instruction for two codes), and the query row is multiplied by a power of two
 // that puts its largest element in [2^7, 2^8), so BF16 queries are exact too down to
 // 2^-21 of their row's maximum. A non-finite query makes its row's outputs NaN.
@@ -43,7 +44,7 @@ constexpr uint32_t kWarps = 4, kThreads = 32 * kWarps;
 constexpr uint32_t kRows = 16;                 // query rows of a tile (MMA M)
 constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (two n8 tiles; MMA K of the second product)
 constexpr uint32_t kUnitKeys = kWarps * kStepKeys;
-constexpr float kPBits = 15.f;                 // P is held times 2^15
+constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
 
 template <uint32_t DP>
 struct Cfg {
@@ -77,28 +78,18 @@ __device__ __forceinline__ uint64_t seq_units(const AttnArgs& p, uint32_t b, boo
     return static_cast<uint64_t>(it.tiles) * it.units * p.c.kv_heads;
 }
 
-// Units of the sequences before `b` and of all (every thread gets both).
-__device__ __forceinline__ void count_units(const AttnArgs& p, uint32_t b, uint64_t* sh, uint64_t& before, uint64_t& all) {
-    uint64_t x = 0, y = 0;
-    for (uint32_t i = threadIdx.x; i < p.b.batch; i += kThreads) {
-        const uint64_t v = seq_units(p, i, false);
-        y += v;
-        if (i < b) x += v;
-    }
+// Units of all sequences (every thread gets the sum).
+__device__ __forceinline__ uint64_t count_units(const AttnArgs& p, uint64_t* sh) {
+    uint64_t x = 0;
+    for (uint32_t i = threadIdx.x; i < p.b.batch; i += kThreads) x += seq_units(p, i, blockIdx.x == 0);
     x = warp_sum(x);
-    y = warp_sum(y);
-    if ((threadIdx.x & 31) == 0) {
-        sh[threadIdx.x >> 5] = x;
-        sh[kWarps + (threadIdx.x >> 5)] = y;
-    }
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
     __syncthreads();
-    before = all = 0;
+    uint64_t all = 0;
 #pragma unroll
-    for (uint32_t w = 0; w < kWarps; ++w) {
-        before += sh[w];
-        all += sh[kWarps + w];
-    }
+    for (uint32_t w = 0; w < kWarps; ++w) all += sh[w];
     __syncthreads();
+    return all;
 }
 
 // The sequence that holds unit `at` (below the total), and its first unit.
@@ -141,19 +132,20 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// `bytes` (16, 8 or 0) bytes global -> shared; the rest of the piece is zero filled.
+// A piece of 16 or 8 bytes global -> shared, or zeros (from an address that is read nothing of).
 template <uint32_t PIECE>
-__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, bool take) {
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src) {
+    if constexpr (PIECE == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+template <uint32_t PIECE>
+__device__ __forceinline__ void fill_piece(uint32_t dst, const void* src, const void* safe, bool take) {
+    const void* from = take ? src : safe;
     const uint32_t bytes = take ? PIECE : 0u;
     if constexpr (PIECE == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-template <bool F16>
-__device__ __forceinline__ void store2(uint16_t* dst, float a, float b) {
-    *reinterpret_cast<uint32_t*>(dst) = pack2<F16>(a, b);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -166,12 +158,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    if (blockIdx.x == 0)
-        for (uint32_t i = threadIdx.x; i < p.b.batch; i += kThreads) seq_units(p, i, true);
-    uint64_t total, none;
-    count_units(p, 0, sh, none, total);
-    const uint64_t ctas = active_ctas(total, p.ctas);
-    if (blockIdx.x >= ctas) return;
+    const uint64_t total = count_units(p, sh), ctas = active_ctas(total, p.ctas);
+    zero_keyless(p);
+    if (blockIdx.x >= ctas) {
+        if (threadIdx.x == 0) write_boundary(p.ws, 0, 0, 0, Seq{}, 0, 0, total, ctas);
+        return;
+    }
+    float* const slots = p.ws + boundary_floats(p.ctas);
     uint64_t u = first_unit(blockIdx.x, total, ctas);
     const uint64_t u_end = first_unit(blockIdx.x + 1, total, ctas);
     uint32_t b;
@@ -181,6 +174,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
     const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
     float* const merge = reinterpret_cast<float*>(smem + warp * C::kStages * C::kStageBytes);
     const uint32_t D = p.c.head_dim;
+    const uint32_t ts = static_cast<uint32_t>(p.c.token_stride);   // below 2^22: a page's tokens within 32 bits
+    uint32_t k_dim[C::kKChunks], v_dim[C::kVPieces];
+#pragma unroll
+    for (uint32_t i = 0; i < C::kKChunks; ++i) k_dim[i] = min(i * 64 + c * 16, D - 16);
+#pragma unroll
+    for (uint32_t i = 0; i < C::kVPieces; ++i) v_dim[i] = min(g * C::kVPiece + i * 8 * C::kVPiece, D - C::kVPiece);
     bool first_part = true;
 
     while (u < u_end) {
@@ -239,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
             bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
             bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
             const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
-            row_scale[r] = rs.scale;
+            // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
+            row_scale[r] = bad ? rs.scale : fmaxf(rs.scale, kMinRowScale);
 #pragma unroll
             for (uint32_t i = 0; i < C::kKChunks; ++i)
 #pragma unroll
@@ -258,56 +258,66 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
 
         // ---- this warp's steps: 16 keys of each unit
         const int key0 = static_cast<int>(unit0 * kUnitKeys + warp * kStepKeys);
-        int meta_page = 0;
-        float meta_k = 0.f, meta_v = 1.f, cur_k = 0.f, cur_v = 1.f;   // lane l: steps l mod 32 of a batch of 32
+        // Lane l holds what step l (mod 32) of a batch of 32 needs; a batch is asked for 32 - kStages + 1
+        // steps before its first use, and its scales are first touched there.
+        int meta_page = -1;
+        float meta_k = 1.f, meta_v = 1.f, cur_k = 1.f, cur_lv = 0.f, cur_iv = 1.f;
         const auto load_meta = [&](uint32_t step) {
             const int key = key0 + static_cast<int>((step + lane) * kUnitKeys);
             meta_page = -1;
-            meta_k = 0.f;
-            meta_v = 1.f;
+            meta_k = meta_v = 1.f;
             if (step + lane < nunits && key < tile_end) {
                 const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
-                if (page < 0 || page >= static_cast<int>(p.c.num_pages)) {
+                if (static_cast<uint32_t>(page) >= p.c.num_pages) {
                     record_failure(&g_kv_attn_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(page));
                 } else {
                     const int64_t at = static_cast<int64_t>(page) * p.c.scale_page_stride + static_cast<int64_t>(h) * p.c.scale_head_stride;
                     meta_page = page;
                     meta_k = p.c.k_scale[at];
                     meta_v = p.c.v_scale[at];
-                    if (meta_k < kMinScale) meta_k = kMinScale;
-                    if (meta_v < kMinScale) meta_v = kMinScale;
                 }
             }
         };
+        // Chunks past the head repeat its last one (their queries are zero, their outputs are not stored).
+        const uint8_t* const k_head = static_cast<const uint8_t*>(p.c.k_codes) + static_cast<int64_t>(h) * p.c.head_stride;
+        const uint8_t* const v_head = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(h) * p.c.head_stride;
         const auto issue = [&](uint32_t step) {
             if (step < nunits) {
                 if ((step & 31u) == 0u) load_meta(step);
                 const int page = __shfl_sync(0xFFFFFFFFu, meta_page, step & 31u);
                 const int key = key0 + static_cast<int>(step * kUnitKeys);
-                const uint32_t slot = ring + (step % C::kStages) * C::kStageBytes;
-                const int64_t off = static_cast<int64_t>(max(page, 0)) * p.c.page_stride + static_cast<int64_t>(h) * p.c.head_stride +
-                                    static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
-                const uint8_t* kp = static_cast<const uint8_t*>(p.c.k_codes) + off;
-                const uint8_t* vp = static_cast<const uint8_t*>(p.c.v_codes) + off;
-                const int left = page < 0 ? 0 : tile_end - key;   // keys of the step that exist
+                const uint32_t slot = ring + (step % C::kStages) * C::kStageBytes + lane * 16, vslot = ring + (step % C::kStages) * C::kStageBytes + kStepKeys * DP + lane * C::kVPiece;
+                const int64_t off = static_cast<int64_t>(page) * p.c.page_stride +
+                                    static_cast<uint32_t>(key & static_cast<int>(p.c.page_size - 1)) * ts;
+                const uint8_t *kp = k_head + off, *vp = v_head + off;
+                if (page >= 0 && tile_end - key >= static_cast<int>(kStepKeys)) {
 #pragma unroll
-                for (uint32_t j = 0; j < 2; ++j)
+                    for (uint32_t j = 0; j < 2; ++j)
 #pragma unroll
-                    for (uint32_t i = 0; i < C::kKChunks; ++i) {
-                        const uint32_t n = 8 * j + g, d = i * 64 + c * 16;
-                        const bool take = static_cast<int>(n) < left && d < D;
-                        copy_piece<16>(slot + ((j * C::kKChunks + i) * 32 + lane) * 16,
-                                       take ? kp + static_cast<int64_t>(n) * p.c.token_stride + d : p.c.k_codes, take);
-                    }
+                        for (uint32_t i = 0; i < C::kKChunks; ++i)
+                            copy_piece<16>(slot + (j * C::kKChunks + i) * 512, kp + ((8 * j + g) * ts + k_dim[i]));
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
+                    for (uint32_t j = 0; j < 4; ++j)
 #pragma unroll
-                    for (uint32_t i = 0; i < C::kVPieces; ++i) {
-                        const uint32_t n = 8 * (j >> 1) + 2 * c + (j & 1), d = g * C::kVPiece + i * 8 * C::kVPiece;
-                        const bool take = static_cast<int>(n) < left && d < D;
-                        copy_piece<C::kVPiece>(slot + kStepKeys * DP + ((j * C::kVPieces + i) * 32 + lane) * C::kVPiece,
-                                               take ? vp + static_cast<int64_t>(n) * p.c.token_stride + d : p.c.v_codes, take);
-                    }
+                        for (uint32_t i = 0; i < C::kVPieces; ++i)
+                            copy_piece<C::kVPiece>(vslot + (j * C::kVPieces + i) * 32 * C::kVPiece,
+                                                   vp + ((8 * (j >> 1) + 2 * c + (j & 1)) * ts + v_dim[i]));
+                } else {
+                    const int left = page < 0 ? 0 : tile_end - key;   // keys of the step that exist; the others are zero filled
+#pragma unroll 1
+                    for (uint32_t j = 0; j < 2; ++j)
+#pragma unroll
+                        for (uint32_t i = 0; i < C::kKChunks; ++i)
+                            fill_piece<16>(slot + (j * C::kKChunks + i) * 512, kp + ((8 * j + g) * ts + k_dim[i]), p.c.k_codes,
+                                           static_cast<int>(8 * j + g) < left);
+#pragma unroll 1
+                    for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+                        for (uint32_t i = 0; i < C::kVPieces; ++i)
+                            fill_piece<C::kVPiece>(vslot + (j * C::kVPieces + i) * 32 * C::kVPiece,
+                                                   vp + ((8 * (j >> 1) + 2 * c + (j & 1)) * ts + v_dim[i]), p.c.v_codes,
+                                                   static_cast<int>(8 * (j >> 1) + 2 * c + (j & 1)) < left);
+                }
             }
             cp_async_commit();
         };
@@ -322,13 +332,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
         for (uint32_t step = 0; step < nunits; ++step) {
             cp_async_wait_group<C::kStages - 2>();
             if ((step & 31u) == 0u) {   // the batch of 32 that the copies have reached
-                cur_k = meta_k;
-                cur_v = meta_v;
+                cur_k = meta_k < kMinScale ? kMinScale : meta_k;
+                const float v = meta_v < kMinScale ? kMinScale : meta_v;
+                cur_lv = __log2f(v);
+                cur_iv = __frcp_rn(v);
             }
             issue(step + C::kStages - 1);
             const int key = key0 + static_cast<int>(step * kUnitKeys);
             if (key >= tile_end) continue;
-            const float ks = __shfl_sync(0xFFFFFFFFu, cur_k, step & 31u), vs = __shfl_sync(0xFFFFFFFFu, cur_v, step & 31u);
+            const float ks = __shfl_sync(0xFFFFFFFFu, cur_k, step & 31u), lv = __shfl_sync(0xFFFFFFFFu, cur_lv, step & 31u),
+                        iv = __shfl_sync(0xFFFFFFFFu, cur_iv, step & 31u);
             const uint8_t* slot = smem + warp * C::kStages * C::kStageBytes + (step % C::kStages) * C::kStageBytes;
 
             // ---- scores
@@ -350,25 +363,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
             }
             // ---- weights
             const bool edge = key + static_cast<int>(kStepKeys) > tile_min;
-            const float lv = __log2f(vs), iv = __frcp_rn(vs);
             uint32_t pf[4];
+            float f[2], mx[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float f = ks * row_scale[r];
-                float y[4];
+                f[r] = ks * row_scale[r];
+                if (edge) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        y[2 * j + e] = fmaf(s[j][2 * r + e], f, lv);
-                        if (edge && key + 8 * j + 2 * static_cast<int>(c) + e >= row_end[r]) y[2 * j + e] = -INFINITY;
-                    }
-                float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                const float m_new = fmaxf(m[r], mx);
-                const float ref = m_new == -INFINITY ? 0.f : m_new - kPBits;
-                if (__any_sync(0xFFFFFFFFu, m_new != m[r])) {
+                        for (int e = 0; e < 2; ++e)
+                            if (key + 8 * j + 2 * static_cast<int>(c) + e >= row_end[r]) s[j][2 * r + e] = -INFINITY;
+                }
+                // f > 0: the largest score gives the largest y = score f + log2(vs)
+                mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 1));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 2));
+                mx[r] = fmaf(mx[r], f[r], lv);
+            }
+            if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] + kRise || mx[1] > m[1] + kRise)) {
+                // a running maximum is exceeded by more than 2^8: it moves, sums and outputs are rescaled
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float m_new = fmaxf(m[r], mx[r]);
                     const float a = m[r] == -INFINITY ? 0.f : ex2(m[r] - m_new);
                     l[r] *= a;
 #pragma unroll
@@ -378,8 +395,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
                     }
                     m[r] = m_new;
                 }
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = ex2(y[e] - ref);
+            for (int r = 0; r < 2; ++r) {
+                const float t = m[r] == -INFINITY ? 0.f : lv - m[r] + kPBits;
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = ex2(fmaf(s[e >> 1][2 * r + (e & 1)], f[r], t));
                 l[r] = fmaf((y[0] + y[1]) + (y[2] + y[3]), iv, l[r]);
                 pf[r] = pack2<true>(y[0], y[1]);
                 pf[2 + r] = pack2<true>(y[2], y[3]);
@@ -484,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
                                         o[i * C::kVPiece + k + 2][2 * r + e], o[i * C::kVPiece + k + 3][2 * r + e]);
         __syncthreads();
         const bool whole = nunits == it.units;
-        float* slot_ws = p.ws + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * slot_floats(DP);
+        if (first_part && threadIdx.x == 0) write_boundary(p.ws, u, u - unit0, it.units, seq, h, item % it.tiles, total, ctas);
+        float* slot_ws = slots + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * slot_floats(DP);
         for (uint32_t i = threadIdx.x; i < kRows * DP / 4; i += kThreads) {
             const uint32_t r = i / (DP / 4), d = (i % (DP / 4)) * 4;
             if (row0 + r >= nrows || d >= D) continue;
@@ -523,50 +546,50 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
     }
 }
 
-// Joins the parts of split items in key order, a CTA per query row; rows whose
-// sequence has no keys become zero.
-template <bool F16>
-__global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p, uint32_t dp) {
-    __shared__ uint64_t sh[2 * kWarps];
+// Joins the parts of split items in key order: a block per boundary between CTAs' ranges and
+// kWarps rows, a warp a row, the parts' loads in flight together.
+template <bool F16, uint32_t DP>
+__global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t n = blockIdx.x / p.q.heads, head = blockIdx.x % p.q.heads;
-    const uint32_t b = seq_of_row(p.b, n);
-    const Seq seq = sequence(p.b, p.c.page_size, b);
-    const int t = static_cast<int>(n) - seq.first;
-    if (t < 0 || t >= seq.count) return;   // a row that no sequence claims
-    const Items it = items_of(p, seq);
-    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(n) * p.out.token_stride + static_cast<int64_t>(head) * p.out.head_stride;
-    if (it.units == 0) {
-        for (uint32_t d = threadIdx.x; d < p.c.head_dim; d += kThreads) dst[d] = 0;
-        return;
-    }
-    uint64_t before, total;
-    count_units(p, b, sh, before, total);
-    const uint32_t h = head / p.group, row = static_cast<uint32_t>(t) * p.group + head % p.group;
-    const uint64_t u0 = before + (static_cast<uint64_t>(h) * it.tiles + row / kRows) * it.units;
-    const uint64_t ctas = active_ctas(total, p.ctas);
-    const uint32_t c0 = cta_of(u0, total, ctas), c1 = cta_of(u0 + it.units - 1, total, ctas);
-    if (c0 == c1) return;   // whole: already written
-    const uint32_t stride = slot_floats(dp), r = row % kRows;
-    // CTA c0's part is its second one unless its range begins inside the item
-    const uint32_t first_slot = first_unit(c0, total, ctas) >= u0 ? 2 * c0 : 2 * c0 + 1;
-    const auto slot = [&](uint32_t cta) { return p.ws + static_cast<uint64_t>(cta == c0 ? first_slot : 2 * cta) * stride; };
-    float mm = -INFINITY;
-    for (uint32_t cta = c0; cta <= c1; ++cta) mm = fmaxf(mm, slot(cta)[kRows * dp + r]);
-    for (uint32_t d = threadIdx.x; d < p.c.head_dim; d += kThreads) {
-        float acc = 0.f, l = 0.f;
-#pragma unroll 4
-        for (uint32_t cta = c0; cta <= c1; ++cta) {
-            const float* s = slot(cta);
-            const float sm = s[kRows * dp + r];
-            const float a = sm == -INFINITY ? 0.f : ex2(sm - mm);
-            acc = fmaf(a, s[r * dp + d], acc);
-            l = fmaf(a, s[kRows * dp + kRows + r], l);
+    const uint32_t c = blockIdx.x + 1, lane = threadIdx.x & 31, r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+    const Boundary b = reinterpret_cast<const Boundary*>(p.ws)[c];
+    const uint32_t row = b.tile * kRows + r;
+    if (b.parts == 0 || row >= static_cast<uint32_t>(b.count) * p.group) return;
+    const float* const slots = p.ws + boundary_floats(p.ctas);
+    const auto slot = [&](uint32_t i) { return slots + static_cast<uint64_t>(i == 0 ? b.slot : 2 * (c + i - 1)) * slot_floats(DP); };
+    float m = -INFINITY;
+    for (uint32_t i = lane; i < b.parts; i += 32) m = fmaxf(m, slot(i)[kRows * DP + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    constexpr uint32_t V = DP / 32;   // consecutive dims of a lane
+    float acc[V] = {}, l = 0.f;
+#pragma unroll 8
+    for (uint32_t i = 0; i < b.parts; ++i) {
+        const float* s = slot(i);
+        const float mi = s[kRows * DP + r];
+        const float a = mi == -INFINITY ? 0.f : ex2(mi - m);
+        l = fmaf(a, s[kRows * DP + kRows + r], l);
+        float x[V];
+        if constexpr (V == 2) {
+            const float2 t = *reinterpret_cast<const float2*>(s + r * DP + 2 * lane);
+            x[0] = t.x, x[1] = t.y;
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < V; k += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(s + r * DP + V * lane + k);
+                x[k] = t.x, x[k + 1] = t.y, x[k + 2] = t.z, x[k + 3] = t.w;
+            }
         }
-        const float y = l == 0.f ? 0.f : acc / l;
-        dst[d] = static_cast<uint16_t>(pack2<F16>(y, 0.f));
+#pragma unroll
+        for (uint32_t k = 0; k < V; ++k) acc[k] = fmaf(a, x[k], acc[k]);
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(b.first + static_cast<int>(row / p.group)) * p.out.token_stride +
+                    static_cast<int64_t>(b.h * p.group + row % p.group) * p.out.head_stride;
+#pragma unroll
+    for (uint32_t k = 0; k < V; k += 2)
+        if (V * lane + k < p.c.head_dim) *reinterpret_cast<uint32_t*>(dst + V * lane + k) = pack2<F16>(acc[k] * inv, acc[k + 1] * inv);
 }
 
 template <bool F16, uint32_t DP>
@@ -586,9 +609,11 @@ cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<F16, DP>, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(p.b.tokens * p.q.heads, 1, 1);
+    if (p.ctas < 2) return cudaSuccess;
+    const uint64_t rows = static_cast<uint64_t>(p.b.max_q) * p.group;   // of an item, at most
+    cfg.gridDim = dim3(p.ctas - 1, (static_cast<uint32_t>(rows < kRows ? rows : kRows) + kWarps - 1) / kWarps, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<F16>, p, DP);
+    return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<F16, DP>, p);
 }
 
 uint32_t padded_dim(uint32_t d) { return d <= 64 ? 64u : d <= 128 ? 128u : 256u; }
@@ -599,7 +624,7 @@ uint32_t grid_ctas(uint32_t dp, int sms) { return static_cast<uint32_t>(sms) * (
 uint64_t kv_attn_ws_bytes(uint32_t head_dim, uint32_t rows_per_head, int sms) {
     if (kv_attn_tc_applies(head_dim, rows_per_head)) return kv_attn_tc_ws_bytes(head_dim, sms);
     const uint32_t dp = padded_dim(head_dim);
-    return 8ull * grid_ctas(dp, sms) * slot_floats(dp);
+    return 4 * boundary_floats(grid_ctas(dp, sms)) + 8ull * grid_ctas(dp, sms) * slot_floats(dp);
 }
 
 int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& q,
@@ -609,10 +634,6 @@ int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_
     while ((1u << p.page_shift) < c.page_size) ++p.page_shift;
     const uint32_t dp = padded_dim(c.head_dim);
     p.ctas = grid_ctas(dp, sms);
-    if (static_cast<uint64_t>(b.tokens) * q.heads > 0x7FFFFFFFull) {
-        *err = "cache attention: too many query rows for one launch";
-        return W8A16_ERR_RANGE;
-    }
     const bool f16 = act_dtype == W8A16_ACT_F16;
     const cudaError_t e = kv_attn_tc_applies(c.head_dim, b.max_q * p.group) ? launch_kv_attn_tc(p, f16, sms, s)
                           : dp == 64    ? (f16 ? launch<true, 64>(p, s) : launch<false, 64>(p, s))

@@ -37,6 +37,45 @@ __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t units, uint64_t 
     return static_cast<uint32_t>(((u + 1) * ctas - 1) / units);
 }
 
+// What CTA c's range begins in, written by it at the head of the workspace for the launch
+// that joins split items: `parts` > 0 where it is the first range to begin inside an item,
+// whose parts are then those of CTAs c - 1 (at `slot`) and c .. c + parts - 2 (their first
+// slots).
+struct Boundary {
+    uint32_t parts, slot;
+    int32_t first, count;    // the sequence's rows
+    uint32_t h, tile;        // the item's head and row tile
+};
+__host__ __device__ constexpr uint64_t boundary_floats(uint32_t ctas) { return (ctas * sizeof(Boundary) + 15) / 16 * 4; }
+__device__ __forceinline__ void write_boundary(float* ws, uint64_t u0, uint64_t item_first, uint32_t item_units, const Seq& s,
+                                               uint32_t h, uint32_t tile, uint64_t total, uint64_t ctas) {
+    Boundary b{0, 0, s.first, s.count, h, tile};
+    const uint32_t c = blockIdx.x;
+    if (c < ctas && u0 != item_first) {
+        const uint64_t before = first_unit(c - 1, total, ctas);
+        if (before <= item_first) {
+            b.parts = cta_of(item_first + item_units - 1, total, ctas) - c + 2;
+            b.slot = before == item_first ? 2 * (c - 1) : 2 * (c - 1) + 1;   // that CTA's first part, or its last
+        }
+    }
+    reinterpret_cast<Boundary*>(ws)[c] = b;
+}
+
+// Zeros in the rows of sequences without keys.
+__device__ __forceinline__ void zero_keyless(const AttnArgs& p) {
+    for (uint32_t b = blockIdx.x; b < p.b.batch; b += gridDim.x) {
+        const Seq s = sequence(p.b, p.c.page_size, b);
+        if (s.bad || s.len > 0) continue;
+        const uint32_t per_head = p.c.head_dim / 8, per_row = p.out.heads * per_head;
+        for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(s.count) * per_row; i += blockDim.x) {
+            const uint32_t n = static_cast<uint32_t>(i / per_row), h = static_cast<uint32_t>(i % per_row) / per_head,
+                           d = static_cast<uint32_t>(i % per_head) * 8;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(s.first + static_cast<int>(n)) * p.out.token_stride +
+                                      static_cast<int64_t>(h) * p.out.head_stride + d) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -46,6 +85,7 @@ __device__ __forceinline__ float ex2(float x) {
 // The row scale of a query: softmax scale times 2^(E - 7) for its largest element's
 // exponent E, and the two factors f1 f2 = 2^(7 - E) that bring the row to [2^7, 2^8)
 // (two: E reaches -133 for BF16 subnormals). A row with a non-finite element gets a NaN scale.
+constexpr float kMinRowScale = 1.3552527156068805e-20f;   // 2^-66
 struct RowScale {
     float scale, f1, f2;
 };

@@ -376,23 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     const uint32_t tm = tl->tmem;
 
     const uint64_t total = total_units<kWarpsAll>(p, sh_units, blockIdx.x == 0);
-    // sequences without keys: their rows are zero
-    for (uint32_t b = blockIdx.x; b < p.b.batch; b += gridDim.x) {
-        const Seq s = sequence(p.b, p.c.page_size, b);
-        if (s.bad || s.len > 0) continue;
-        const uint32_t per_row = p.out.heads * (p.c.head_dim / 8);
-        for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(s.count) * per_row; i += kThreads) {
-            const uint32_t n = static_cast<uint32_t>(i / per_row), h = static_cast<uint32_t>(i % per_row) / (p.c.head_dim / 8),
-                           d = static_cast<uint32_t>(i % (p.c.head_dim / 8)) * 8;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(s.first + static_cast<int>(n)) * p.out.token_stride +
-                                      static_cast<int64_t>(h) * p.out.head_stride + d) = make_uint4(0, 0, 0, 0);
-        }
-    }
+    zero_keyless(p);
     const uint64_t ctas = active_ctas(total, p.ctas);
     const bool works = blockIdx.x < ctas;
     const uint64_t u0 = works ? first_unit(blockIdx.x, total, ctas) : 0, u_end = works ? first_unit(blockIdx.x + 1, total, ctas) : 0;
+    float* const slots = p.ws + boundary_floats(p.ctas);
+    if (!works && threadIdx.x == 0) write_boundary(p.ws, 0, 0, 0, Seq{}, 0, 0, total, ctas);
     if (works) {
         Item it = find_item<kWarpsAll>(p, u0, sh_units);
+        if (threadIdx.x == 0) write_boundary(p.ws, u0, it.first, it.n, it.s, it.h, it.rb, total, ctas);
         uint64_t u = u0;
 
         if (warp < kSoftmaxWarps) {
@@ -437,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         }
                         const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
                         // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
-                        rowf = bad ? rs.scale : fmaxf(rs.scale, 1.3552527156068805e-20f);
+                        rowf = bad ? rs.scale : fmaxf(rs.scale, kMinRowScale);
 #pragma unroll
                         for (uint32_t un = 0; un < DP / 8; ++un) {
                             uint32_t o[4];
@@ -515,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     tc_fence_after();
                     // ---- outputs, or this range's part of them ([d][row], coalesced over rows)
                     const bool whole = cnt == it.n;
-                    float* slot = p.ws + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * ((DP + 2) * kItemRows);
+                    float* slot = slots + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * ((DP + 2) * kItemRows);
                     const bool none = l == 0.f;   // a row that sees no key is zero
                     const float inv = none ? 0.f : 1.f / l;
                     const auto norm = [&](uint32_t x) { return __uint_as_float(x) * inv; };
@@ -787,32 +779,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     if (warp == kIssueWarp) tmem_dealloc(tm, 512);
 }
 
-// Joins the parts of split items in key order. blockIdx.x = c - 1 for the boundary before
-// CTA c's range, which does the item if it is the first boundary inside it;
-// blockIdx.y = 16 dims, a thread a row.
+// Joins the parts of split items in key order: a block per boundary between CTAs' ranges and
+// 16 dims, a thread per row.
 constexpr uint32_t kJoinThreads = kItemRows, kJoinDims = 16;
 template <bool F16>
 __global__ void __launch_bounds__(kJoinThreads) kv_attn_tc_join_kernel(const AttnArgs p, uint32_t dp) {
-    __shared__ uint64_t sh_units[kChunk];
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint64_t total = total_units<kJoinThreads / 32>(p, sh_units, false);
-    const uint64_t ctas = active_ctas(total, p.ctas);
     const uint32_t c = blockIdx.x + 1, d0 = blockIdx.y * kJoinDims;
-    if (c >= ctas || d0 >= p.c.head_dim) return;
-    const uint64_t u = first_unit(c, total, ctas);
-    const Item it = find_item<kJoinThreads / 32>(p, u, sh_units);
-    if (it.first == u || first_unit(c - 1, total, ctas) > it.first) return;
-    const uint32_t c0 = c - 1, c1 = cta_of(it.first + it.n - 1, total, ctas);
-    const uint32_t row = threadIdx.x, r = it.rb * kItemRows + row;
-    if (r >= static_cast<uint32_t>(it.s.count) * p.group) return;
+    const Boundary b = reinterpret_cast<const Boundary*>(p.ws)[c];
+    const uint32_t row = threadIdx.x, r = b.tile * kItemRows + row;
+    if (b.parts == 0 || r >= static_cast<uint32_t>(b.count) * p.group) return;
     const uint64_t stride = static_cast<uint64_t>(dp + 2) * kItemRows;
-    const uint64_t slot0 = first_unit(c0, total, ctas) == it.first ? 2ull * c0 : 2ull * c0 + 1;   // c0's first part, or its last
-    const auto slot = [&](uint32_t cta) { return p.ws + (cta == c0 ? slot0 : 2ull * cta) * stride; };
+    const float* const slots = p.ws + boundary_floats(p.ctas);
+    const auto slot = [&](uint32_t i) { return slots + (i == 0 ? b.slot : 2ull * (c + i - 1)) * stride; };
     float m = -INFINITY;
-    for (uint32_t i = c0; i <= c1; ++i) m = fmaxf(m, slot(i)[dp * kItemRows + row]);
+    for (uint32_t i = 0; i < b.parts; ++i) m = fmaxf(m, slot(i)[dp * kItemRows + row]);
     float acc[kJoinDims] = {}, l = 0.f;
-    for (uint32_t i = c0; i <= c1; ++i) {
+    for (uint32_t i = 0; i < b.parts; ++i) {
         const float* s = slot(i);
         const float mi = s[dp * kItemRows + row];
         const float a = mi == -INFINITY ? 0.f : ex2(mi - m);
@@ -821,8 +805,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_tc_join_kernel(const Att
         for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] = fmaf(a, s[(d0 + d) * kItemRows + row], acc[d]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(r / p.group)) * p.out.token_stride +
-                    static_cast<int64_t>(it.h * p.group + r % p.group) * p.out.head_stride + d0;
+    uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(b.first + static_cast<int>(r / p.group)) * p.out.token_stride +
+                    static_cast<int64_t>(b.h * p.group + r % p.group) * p.out.head_stride + d0;
     uint32_t w[kJoinDims / 2];
 #pragma unroll
     for (uint32_t d = 0; d < kJoinDims / 2; ++d) w[d] = pack2<F16>(acc[2 * d] * inv, acc[2 * d + 1] * inv);
@@ -859,7 +843,7 @@ cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
 bool kv_attn_tc_applies(uint32_t head_dim, uint32_t rows_per_head) { return head_dim <= 128 && rows_per_head >= 64; }
 
 uint64_t kv_attn_tc_ws_bytes(uint32_t head_dim, int sms) {
-    return 8ull * static_cast<uint32_t>(sms) * ((head_dim <= 64 ? 64u : 128u) + 2) * kItemRows;
+    return 4 * boundary_floats(static_cast<uint32_t>(sms)) + 8ull * static_cast<uint32_t>(sms) * ((head_dim <= 64 ? 64u : 128u) + 2) * kItemRows;
 }
 
 cudaError_t launch_kv_attn_tc(AttnArgs p, bool f16, int sms, cudaStream_t s) {

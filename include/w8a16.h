@@ -341,8 +341,8 @@ enum {
  *       * k_scale[page*scale_page_stride + head*scale_head_stride].
  * The strides are byte counts for the codes, element counts for the scales, and
  * shared by K and V, so pages may be laid out [page][head][slot][d] or
- * [page][slot][head][d]. Codes 16-byte aligned, code strides multiples of 16;
- * page_size a power of two in 16..256; head_dim a multiple of 16 in 16..256. */
+ * [page][slot][head][d]. Codes 16-byte aligned, code strides multiples of 16,
+ * token_stride at most 2^22; page_size a power of two in 16..256; head_dim a multiple of 16 in 16..256. */
 typedef struct {
     void *k_codes, *v_codes;
     float *k_scale, *v_scale;
