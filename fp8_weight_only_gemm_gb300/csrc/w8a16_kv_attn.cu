@@ -14,12 +14,14 @@
 // that puts its largest element in [2^7, 2^8), so BF16 queries are exact too down to
 // 2^-21 of their row's maximum. A non-finite query makes its row's outputs NaN.
 //
-// Layout. The products are m16n8k16 with 16 query rows (the G query heads of one
-// key/value head times the call's tokens) as M. The order of a contraction's index and of
-// an output's columns is free, and both are chosen so that every thread reads 16
-// consecutive codes of a key (16, or DP / 8, of a value) and nobody else reads them: a
-// thread copies its own fragments with cp.async into a slot of its own, a ring that
-// needs no barrier at all.
+// Layout. The products are m16n8k16 with the cache as M: S^T = K Q^T for 16 keys and 8
+// query rows (the G query heads of one key/value head times the call's tokens), O^T = V^T P^T,
+// so up to 8 rows waste nothing, and 9 to 16 use each converted operand twice. The order of a
+// contraction's index and of an output's rows is free, and both are chosen so that every
+// thread reads 16 consecutive codes of a key (16, or DP / 8, of a value): only P is
+// transposed between the products (movmatrix). A warp's step is 16 keys, copied by the bulk
+// copy engine into a ring of its own: two copies where a page's tokens are contiguous,
+// else one a row.
 //
 // Work. The units (64 keys of one sequence, key/value head and 16-row tile) of the whole
 // call, in that order, are split over the grid in equal contiguous ranges, so ragged
@@ -41,26 +43,29 @@ namespace {
 __device__ DeviceStatus g_kv_attn_status;
 
 constexpr uint32_t kWarps = 4, kThreads = 32 * kWarps;
-constexpr uint32_t kRows = 16;                 // query rows of a tile (MMA M)
-constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (two n8 tiles; MMA K of the second product)
+constexpr uint32_t kMaxRows = 16;              // query rows of a tile: 8 NR
+constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (MMA M of the first product, K of the second)
 constexpr uint32_t kUnitKeys = kWarps * kStepKeys;
 constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
 
-template <uint32_t DP>
+// DP: the head size rounded up to 64, 128 or 256. NR: tiles of 8 query rows, 1 or 2.
+template <uint32_t DP, uint32_t NR>
 struct Cfg {
-    static constexpr uint32_t kStages = DP >= 256 ? 3 : 4;
-    static constexpr uint32_t kCtasPerSm = DP >= 256 ? 2 : 3;
+    static constexpr uint32_t kRows = 8 * NR;
+    static constexpr uint32_t kStages = 3;
+    static constexpr uint32_t kCtasPerSm = DP >= 256 ? 2 : NR == 2 ? 3 : 4;   // by registers, and shared memory for 256
     static constexpr uint32_t kKChunks = DP / 64;             // 16-byte chunks of a key row per thread
     static constexpr uint32_t kVBytes = DP / 8;               // bytes of a value row per thread
     static constexpr uint32_t kVPiece = kVBytes < 16 ? kVBytes : 16;
     static constexpr uint32_t kVPieces = kVBytes / kVPiece;
     static constexpr uint32_t kStageBytes = 2 * kStepKeys * DP;
-    static constexpr uint32_t kSmem = kWarps * kStages * kStageBytes;
+    static constexpr uint32_t kSmem = kWarps * kStages * kStageBytes;   // (rows of the head's own size, at most DP)
     static_assert(kStages * kStageBytes >= kRows * DP * 4, "a warp's outputs fit its ring");
 };
+constexpr uint32_t kMostCtasPerSm = 4;
 
-// Workspace: slot (cta, which) = [kRows][DP] outputs, [kRows] maxima, [kRows] sums.
-__host__ __device__ constexpr uint32_t slot_floats(uint32_t dp) { return kRows * dp + 2 * kRows; }
+// Workspace: slot (cta, which) = [kMaxRows][DP] outputs, [kMaxRows] maxima, [kMaxRows] sums.
+__host__ __device__ constexpr uint32_t slot_floats(uint32_t dp) { return kMaxRows * dp + 2 * kMaxRows; }
 
 // ------------------------------------------------------------ the schedule --
 struct Items {
@@ -69,7 +74,7 @@ struct Items {
 };
 __device__ __forceinline__ Items items_of(const AttnArgs& p, const Seq& s) {
     const uint32_t len = static_cast<uint32_t>(max(s.len, 0));
-    return {(static_cast<uint32_t>(s.count) * p.group + kRows - 1) / kRows, (len + kUnitKeys - 1) / kUnitKeys};
+    return {(static_cast<uint32_t>(s.count) * p.group + p.tile_rows - 1) / p.tile_rows, (len + kUnitKeys - 1) / kUnitKeys};
 }
 __device__ __forceinline__ uint64_t seq_units(const AttnArgs& p, uint32_t b, bool report) {
     const Seq s = sequence(p.b, p.c.page_size, b);
@@ -132,29 +137,34 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// A piece of 16 or 8 bytes global -> shared, or zeros (from an address that is read nothing of).
-template <uint32_t PIECE>
-__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src) {
-    if constexpr (PIECE == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
-template <uint32_t PIECE>
-__device__ __forceinline__ void fill_piece(uint32_t dst, const void* src, const void* safe, bool take) {
-    const void* from = take ? src : safe;
-    const uint32_t bytes = take ? PIECE : 0u;
-    if constexpr (PIECE == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
+    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_status, 1);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // ----------------------------------------------------------------- kernel --
-template <bool F16, uint32_t DP>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(const AttnArgs p) {
-    using C = Cfg<DP>;
+template <bool F16, uint32_t DP, uint32_t NR>
+__global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_kernel(const AttnArgs p) {
+    using C = Cfg<DP, NR>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sh[2 * kWarps];
-    __shared__ float sh_m[kWarps][kRows], sh_l[kWarps][kRows];
+    __shared__ float sh_m[kWarps][C::kRows], sh_l[kWarps][C::kRows];
+    __shared__ uint64_t full[kWarps][C::kStages];
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kWarps * C::kStages; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -171,15 +181,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
     uint64_t base;
     find_unit(p, u, sh, b, base);
 
-    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
-    float* const merge = reinterpret_cast<float*>(smem + warp * C::kStages * C::kStageBytes);
+    uint8_t* const ring = smem + warp * C::kStages * C::kStageBytes;
+    float* const merge = reinterpret_cast<float*>(ring);
     const uint32_t D = p.c.head_dim;
-    const uint32_t ts = static_cast<uint32_t>(p.c.token_stride);   // below 2^22: a page's tokens within 32 bits
-    uint32_t k_dim[C::kKChunks], v_dim[C::kVPieces];
+    const uint32_t ts = static_cast<uint32_t>(p.c.token_stride);   // at most 2^22: a page's tokens within 32 bits
+    uint32_t k_at[C::kKChunks], v_at[C::kVPieces];   // this thread's bytes of a step: chunks past the head repeat its last
 #pragma unroll
-    for (uint32_t i = 0; i < C::kKChunks; ++i) k_dim[i] = min(i * 64 + c * 16, D - 16);
+    for (uint32_t i = 0; i < C::kKChunks; ++i) k_at[i] = g * D + min(i * 64 + c * 16, D - 16);
 #pragma unroll
-    for (uint32_t i = 0; i < C::kVPieces; ++i) v_dim[i] = min(g * C::kVPiece + i * 8 * C::kVPiece, D - C::kVPiece);
+    for (uint32_t i = 0; i < C::kVPieces; ++i) v_at[i] = (kStepKeys + 2 * c) * D + min(g * C::kVPiece + i * 8 * C::kVPiece, D - C::kVPiece);
+    uint32_t taken = 0;   // steps of this warp so far
     bool first_part = true;
 
     while (u < u_end) {
@@ -196,25 +207,72 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
         const uint32_t item = static_cast<uint32_t>(in_seq / it.units);
         const uint32_t unit0 = static_cast<uint32_t>(in_seq % it.units);
         const uint32_t nunits = static_cast<uint32_t>(min(static_cast<uint64_t>(it.units - unit0), u_end - u));
-        const uint32_t h = item / it.tiles, row0 = (item % it.tiles) * kRows;
+        const uint32_t h = item / it.tiles, row0 = (item % it.tiles) * C::kRows;
         const uint32_t nrows = static_cast<uint32_t>(seq.count) * p.group;
+        const int before = seq.len - seq.count + 1;   // keys that the sequence's first token sees
+        // keys that any row, and every row, of the tile sees
+        const int tile_end = before + static_cast<int>((min(row0 + C::kRows, nrows) - 1) / p.group),
+                  tile_min = before + static_cast<int>(row0 / p.group);
 
-        // ---- the query tile: rows g and g + 8 of it, FP16, each times 2^(7 - exponent of its maximum)
-        uint32_t qf[C::kKChunks][4][4];
-        float row_scale[2];
-        int row_end[2];   // keys that the row sees
+        // ---- this warp's steps: 16 keys of each unit
+        const int key0 = static_cast<int>(unit0 * kUnitKeys + warp * kStepKeys);
+        const uint32_t nsteps = static_cast<uint32_t>(max(0, min(static_cast<int>(nunits), (tile_end - key0 + static_cast<int>(kUnitKeys) - 1) / static_cast<int>(kUnitKeys))));
+        // Lane l holds what step l (mod 32) of a batch of 32 needs; a batch is asked for kStages - 1
+        // steps before its first use, and its scales are first touched there.
+        int meta_page = 0;
+        float meta_k = 1.f, meta_v = 1.f, cur_k = 1.f, cur_lv = 0.f, cur_iv = 1.f;
+        const auto load_meta = [&](uint32_t step) {
+            const int key = key0 + static_cast<int>((step + lane) * kUnitKeys);
+            meta_page = 0;
+            meta_k = meta_v = 1.f;
+            if (step + lane < nsteps) {
+                const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
+                if (static_cast<uint32_t>(page) >= p.c.num_pages) {   // page 0 instead
+                    record_failure(&g_kv_attn_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(page));
+                } else {
+                    const int64_t at = static_cast<int64_t>(page) * p.c.scale_page_stride + static_cast<int64_t>(h) * p.c.scale_head_stride;
+                    meta_page = page;
+                    meta_k = p.c.k_scale[at];
+                    meta_v = p.c.v_scale[at];
+                }
+            }
+        };
+        // This lane's source: K for lane 0 (or lanes 0-15, a row each), V for lane 1 (or 16-31).
+        // Keys past the last one repeat it: their scores are masked, and their values are as finite as
+        // those that they repeat (where rows see different keys: see below).
+        const auto issue = [&](uint32_t step) {
+            if (step >= nsteps) return;
+            if ((step & 31u) == 0u) load_meta(step);
+            const int page = __shfl_sync(0xFFFFFFFFu, meta_page, step & 31u);
+            const int key = key0 + static_cast<int>(step * kUnitKeys);
+            const uint32_t at = (taken + step) % C::kStages, slot = smem_u32(ring) + at * C::kStageBytes, bar = smem_u32(&full[warp][at]);
+            const bool block = ts == D && tile_end - key >= static_cast<int>(kStepKeys);
+            const uint8_t* src = static_cast<const uint8_t*>((block ? lane & 1u : lane & 16u) ? p.c.v_codes : p.c.k_codes) +
+                                 static_cast<int64_t>(h) * p.c.head_stride + static_cast<int64_t>(page) * p.c.page_stride +
+                                 static_cast<uint32_t>(key & static_cast<int>(p.c.page_size - 1)) * ts;
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kStepKeys * D);
+            __syncwarp();
+            if (block) {
+                if (lane < 2) bulk_copy(slot + lane * kStepKeys * D, src, kStepKeys * D, bar);
+            } else {
+                bulk_copy(slot + lane * D, src + min(lane & 15u, static_cast<uint32_t>(tile_end - key - 1)) * ts, D, bar);
+            }
+        };
+#pragma unroll 1
+        for (uint32_t s = 0; s < C::kStages - 1; ++s) issue(s);
+
+        // ---- the query tile: row 8 t + g of it, FP16, each times 2^(7 - exponent of its maximum)
+        uint32_t qf[NR][C::kKChunks][4][2];
+        float row_scale[NR][2];   // of rows 8 t + 2 c + e
+        int row_end[NR][2];       // keys that they see
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t row = row0 + g + 8 * r;
+        for (uint32_t t = 0; t < NR; ++t) {
+            const uint32_t row = row0 + 8 * t + g;
             const bool real = row < nrows;
-            const uint32_t t = real ? row / p.group : 0, head = h * p.group + (real ? row % p.group : 0);
-            row_end[r] = real ? seq.len - seq.count + static_cast<int>(t) + 1 : 0x7FFFFFFF;
             const uint16_t* src = static_cast<const uint16_t*>(p.q.ptr) +
-                                  static_cast<int64_t>(seq.first + static_cast<int>(t)) * p.q.token_stride +
-                                  static_cast<int64_t>(head) * p.q.head_stride;
+                                  static_cast<int64_t>(seq.first + static_cast<int>(real ? row / p.group : 0)) * p.q.token_stride +
+                                  static_cast<int64_t>(h * p.group + (real ? row % p.group : 0)) * p.q.head_stride;
             uint32_t raw[C::kKChunks][8];
-            float mx = 0.f;
-            bool finite = true;
 #pragma unroll
             for (uint32_t i = 0; i < C::kKChunks; ++i) {
                 const uint32_t d = i * 64 + c * 16;
@@ -225,243 +283,196 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
                 }
                 raw[i][0] = a.x, raw[i][1] = a.y, raw[i][2] = a.z, raw[i][3] = a.w;
                 raw[i][4] = e.x, raw[i][5] = e.y, raw[i][6] = e.z, raw[i][7] = e.w;
+            }
+            float mx = 0.f;
+            bool finite = true;
+#pragma unroll
+            for (uint32_t i = 0; i < C::kKChunks; ++i)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float2 x = unpack2<F16>(raw[i][k]);
                     finite = finite && fabsf(x.x) <= 3.4028235e38f && fabsf(x.y) <= 3.4028235e38f;
                     mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
                 }
-            }
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            int bad = !finite;
-            bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
-            bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
+            const bool bad = (__ballot_sync(0xFFFFFFFFu, !finite) >> (4 * g) & 15u) != 0u;   // by the row's four lanes
             const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
             // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
-            row_scale[r] = bad ? rs.scale : fmaxf(rs.scale, kMinRowScale);
+            const float mine = bad ? rs.scale : fmaxf(rs.scale, kMinRowScale);
+#pragma unroll
+            for (uint32_t e = 0; e < 2; ++e) {
+                row_scale[t][e] = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * c + e));
+                const uint32_t r = row0 + 8 * t + 2 * c + e;
+                row_end[t][e] = r < nrows ? before + static_cast<int>(r / p.group) : 0x7FFFFFFF;
+            }
 #pragma unroll
             for (uint32_t i = 0; i < C::kKChunks; ++i)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    float2 x = unpack2<F16>(raw[i][k]);
-                    if (bad) x = make_float2(0.f, 0.f);   // the row's scale is NaN
-                    qf[i][k >> 1][(k & 1) * 2 + r] = pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
+                    const float2 x = unpack2<F16>(raw[i][k]);
+                    qf[t][i][k >> 1][k & 1] = bad ? 0u : pack2<true>(x.x * rs.f1 * rs.f2, x.y * rs.f1 * rs.f2);
                 }
         }
-        int tile_end, tile_min;   // keys any row, and every row, of the tile sees
-        {
-            const uint32_t last = min(row0 + kRows, nrows) - 1;
-            tile_end = seq.len - seq.count + static_cast<int>(last / p.group) + 1;
-            tile_min = seq.len - seq.count + static_cast<int>(row0 / p.group) + 1;
-        }
 
-        // ---- this warp's steps: 16 keys of each unit
-        const int key0 = static_cast<int>(unit0 * kUnitKeys + warp * kStepKeys);
-        // Lane l holds what step l (mod 32) of a batch of 32 needs; a batch is asked for 32 - kStages + 1
-        // steps before its first use, and its scales are first touched there.
-        int meta_page = -1;
-        float meta_k = 1.f, meta_v = 1.f, cur_k = 1.f, cur_lv = 0.f, cur_iv = 1.f;
-        const auto load_meta = [&](uint32_t step) {
-            const int key = key0 + static_cast<int>((step + lane) * kUnitKeys);
-            meta_page = -1;
-            meta_k = meta_v = 1.f;
-            if (step + lane < nunits && key < tile_end) {
-                const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
-                if (static_cast<uint32_t>(page) >= p.c.num_pages) {
-                    record_failure(&g_kv_attn_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(page));
-                } else {
-                    const int64_t at = static_cast<int64_t>(page) * p.c.scale_page_stride + static_cast<int64_t>(h) * p.c.scale_head_stride;
-                    meta_page = page;
-                    meta_k = p.c.k_scale[at];
-                    meta_v = p.c.v_scale[at];
-                }
-            }
-        };
-        // Chunks past the head repeat its last one (their queries are zero, their outputs are not stored).
-        const uint8_t* const k_head = static_cast<const uint8_t*>(p.c.k_codes) + static_cast<int64_t>(h) * p.c.head_stride;
-        const uint8_t* const v_head = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(h) * p.c.head_stride;
-        const auto issue = [&](uint32_t step) {
-            if (step < nunits) {
-                if ((step & 31u) == 0u) load_meta(step);
-                const int page = __shfl_sync(0xFFFFFFFFu, meta_page, step & 31u);
-                const int key = key0 + static_cast<int>(step * kUnitKeys);
-                const uint32_t slot = ring + (step % C::kStages) * C::kStageBytes + lane * 16, vslot = ring + (step % C::kStages) * C::kStageBytes + kStepKeys * DP + lane * C::kVPiece;
-                const int64_t off = static_cast<int64_t>(page) * p.c.page_stride +
-                                    static_cast<uint32_t>(key & static_cast<int>(p.c.page_size - 1)) * ts;
-                const uint8_t *kp = k_head + off, *vp = v_head + off;
-                if (page >= 0 && tile_end - key >= static_cast<int>(kStepKeys)) {
+        // O^T: tile mt, rows 2 mt and 2 mt + 1 of this thread's 2 DP / 16 dims
+        float o[NR][DP / 16][4];
 #pragma unroll
-                    for (uint32_t j = 0; j < 2; ++j)
+        for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
-                        for (uint32_t i = 0; i < C::kKChunks; ++i)
-                            copy_piece<16>(slot + (j * C::kKChunks + i) * 512, kp + ((8 * j + g) * ts + k_dim[i]));
+            for (uint32_t n = 0; n < DP / 16; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+        float m[NR][2], l[NR][2];   // of rows 8 t + 2 c + e; l: this lane's keys
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-#pragma unroll
-                        for (uint32_t i = 0; i < C::kVPieces; ++i)
-                            copy_piece<C::kVPiece>(vslot + (j * C::kVPieces + i) * 32 * C::kVPiece,
-                                                   vp + ((8 * (j >> 1) + 2 * c + (j & 1)) * ts + v_dim[i]));
-                } else {
-                    const int left = page < 0 ? 0 : tile_end - key;   // keys of the step that exist; the others are zero filled
+        for (uint32_t t = 0; t < NR; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+
 #pragma unroll 1
-                    for (uint32_t j = 0; j < 2; ++j)
-#pragma unroll
-                        for (uint32_t i = 0; i < C::kKChunks; ++i)
-                            fill_piece<16>(slot + (j * C::kKChunks + i) * 512, kp + ((8 * j + g) * ts + k_dim[i]), p.c.k_codes,
-                                           static_cast<int>(8 * j + g) < left);
-#pragma unroll 1
-                    for (uint32_t j = 0; j < 4; ++j)
-#pragma unroll
-                        for (uint32_t i = 0; i < C::kVPieces; ++i)
-                            fill_piece<C::kVPiece>(vslot + (j * C::kVPieces + i) * 32 * C::kVPiece,
-                                                   vp + ((8 * (j >> 1) + 2 * c + (j & 1)) * ts + v_dim[i]), p.c.v_codes,
-                                                   static_cast<int>(8 * (j >> 1) + 2 * c + (j & 1)) < left);
-                }
-            }
-            cp_async_commit();
-        };
-
-        float o[DP / 8][4];
-#pragma unroll
-        for (uint32_t n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-#pragma unroll
-        for (uint32_t s = 0; s < C::kStages - 1; ++s) issue(s);
-        for (uint32_t step = 0; step < nunits; ++step) {
-            cp_async_wait_group<C::kStages - 2>();
+        for (uint32_t step = 0; step < nsteps; ++step) {
+            const uint32_t at = (taken + step) % C::kStages, parity = ((taken + step) / C::kStages) & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&full[warp][at]), parity) ||
+                                             wait_slow(smem_u32(&full[warp][at]), parity, p.timeout_ns, &abort_flag)))
+                break;
             if ((step & 31u) == 0u) {   // the batch of 32 that the copies have reached
                 cur_k = meta_k < kMinScale ? kMinScale : meta_k;
                 const float v = meta_v < kMinScale ? kMinScale : meta_v;
                 cur_lv = __log2f(v);
                 cur_iv = __frcp_rn(v);
             }
+            // the slot before this one has been read by all lanes: the next copies may overwrite it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             issue(step + C::kStages - 1);
             const int key = key0 + static_cast<int>(step * kUnitKeys);
-            if (key >= tile_end) continue;
             const float ks = __shfl_sync(0xFFFFFFFFu, cur_k, step & 31u), lv = __shfl_sync(0xFFFFFFFFu, cur_lv, step & 31u),
                         iv = __shfl_sync(0xFFFFFFFFu, cur_iv, step & 31u);
-            const uint8_t* slot = smem + warp * C::kStages * C::kStageBytes + (step % C::kStages) * C::kStageBytes;
+            const uint8_t* slot = ring + at * C::kStageBytes;
 
-            // ---- scores
-            float s[2][4];
+            // ---- scores of keys g, g + 8 and rows 2 c, 2 c + 1; two chains of products each
+            float s[NR][4], s2[NR][4];
 #pragma unroll
-            for (uint32_t j = 0; j < 2; ++j) {
-                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
-                for (uint32_t i = 0; i < C::kKChunks; ++i) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(slot + ((j * C::kKChunks + i) * 32 + lane) * 16);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_f16x4(ww[k], b0, b1);
-                        mma_f16(s[j], qf[i][k], b0, b1);
-                    }
+            for (uint32_t i = 0; i < C::kKChunks; ++i) {
+                const uint4 w0 = *reinterpret_cast<const uint4*>(slot + k_at[i]), w1 = *reinterpret_cast<const uint4*>(slot + 8 * D + k_at[i]);
+                const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4];
+                    e4m3x4_to_f16x4(x0[k], a[0], a[2]);
+                    e4m3x4_to_f16x4(x1[k], a[1], a[3]);
+#pragma unroll
+                    for (uint32_t t = 0; t < NR; ++t) mma_f16(k & 1 ? s2[t] : s[t], a, qf[t][i][k][0], qf[t][i][k][1]);
                 }
             }
             // ---- weights
             const bool edge = key + static_cast<int>(kStepKeys) > tile_min;
-            uint32_t pf[4];
-            float f[2], mx[2];
+            float f[NR][2], mx[NR][2];
+            bool rise = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                f[r] = ks * row_scale[r];
-                if (edge) {
+            for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (key + 8 * j + 2 * static_cast<int>(c) + e >= row_end[r]) s[j][2 * r + e] = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    s[t][e] += s2[t][e];
+                    s[t][2 + e] += s2[t][2 + e];
+                    f[t][e] = ks * row_scale[t][e];
+                    if (edge) {
+                        if (key + static_cast<int>(g) >= row_end[t][e]) s[t][e] = -INFINITY;
+                        if (key + 8 + static_cast<int>(g) >= row_end[t][e]) s[t][2 + e] = -INFINITY;
+                    }
+                    // f > 0: the largest score gives the largest y = score f + log2(vs)
+                    float x = fmaxf(s[t][e], s[t][2 + e]);
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    mx[t][e] = fmaf(x, f[t][e], lv);
+                    rise = rise || mx[t][e] > m[t][e] + kRise;
                 }
-                // f > 0: the largest score gives the largest y = score f + log2(vs)
-                mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 1));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 2));
-                mx[r] = fmaf(mx[r], f[r], lv);
-            }
-            if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] + kRise || mx[1] > m[1] + kRise)) {
+            if (__any_sync(0xFFFFFFFFu, rise)) {
                 // a running maximum is exceeded by more than 2^8: it moves, sums and outputs are rescaled
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float m_new = fmaxf(m[r], mx[r]);
-                    const float a = m[r] == -INFINITY ? 0.f : ex2(m[r] - m_new);
-                    l[r] *= a;
+                for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
-                    for (uint32_t n = 0; n < DP / 8; ++n) {
-                        o[n][2 * r] *= a;
-                        o[n][2 * r + 1] *= a;
+                    for (int e = 0; e < 2; ++e) {
+                        const float m_new = fmaxf(m[t][e], mx[t][e]);
+                        const float a = m[t][e] == -INFINITY ? 0.f : ex2(m[t][e] - m_new);
+                        l[t][e] *= a;
+#pragma unroll
+                        for (uint32_t n = 0; n < DP / 16; ++n) {
+                            o[t][n][e] *= a;
+                            o[t][n][2 + e] *= a;
+                        }
+                        m[t][e] = m_new;
                     }
-                    m[r] = m_new;
-                }
             }
+            uint32_t pb[NR][2];   // P^T as the second product's operand: keys 2 c.. of row g
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float t = m[r] == -INFINITY ? 0.f : lv - m[r] + kPBits;
+            for (uint32_t t = 0; t < NR; ++t) {
                 float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = ex2(fmaf(s[e >> 1][2 * r + (e & 1)], f[r], t));
-                l[r] = fmaf((y[0] + y[1]) + (y[2] + y[3]), iv, l[r]);
-                pf[r] = pack2<true>(y[0], y[1]);
-                pf[2 + r] = pack2<true>(y[2], y[3]);
+                for (int e = 0; e < 2; ++e) {
+                    const float d = m[t][e] == -INFINITY ? 0.f : lv - m[t][e] + kPBits;
+                    y[e] = ex2(fmaf(s[t][e], f[t][e], d));
+                    y[2 + e] = ex2(fmaf(s[t][2 + e], f[t][e], d));
+                    l[t][e] = fmaf(y[e] + y[2 + e], iv, l[t][e]);
+                }
+                pb[t][0] = transpose8x8(pack2<true>(y[0], y[1]));
+                pb[t][1] = transpose8x8(pack2<true>(y[2], y[3]));
             }
             // ---- outputs
-            const uint8_t* vslot = slot + kStepKeys * DP;
-            uint32_t vw[4][C::kVBytes / 4];
+            uint32_t vw[4][C::kVBytes / 4];   // keys 2 c, 2 c + 1, 8 + 2 c, 9 + 2 c
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
 #pragma unroll
                 for (uint32_t i = 0; i < C::kVPieces; ++i) {
-                    const uint8_t* at = vslot + ((j * C::kVPieces + i) * 32 + lane) * C::kVPiece;
+                    const uint8_t* from = slot + (8 * (j >> 1) + (j & 1)) * D + v_at[i];
                     if constexpr (C::kVPiece == 16) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(at);
+                        const uint4 w = *reinterpret_cast<const uint4*>(from);
                         vw[j][4 * i] = w.x, vw[j][4 * i + 1] = w.y, vw[j][4 * i + 2] = w.z, vw[j][4 * i + 3] = w.w;
                     } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(at);
+                        const uint2 w = *reinterpret_cast<const uint2*>(from);
                         vw[j][0] = w.x, vw[j][1] = w.y;
                     }
                 }
             if (edge && seq.count > 1) {
                 // keys that some rows do not see: a NaN value there must not reach them through 0 * NaN.
-                // The NaN codes leave the product, and a product of indicators (row sees key, value is
-                // NaN) marks the outputs that are NaN.
+                // The NaN codes leave the product, and a product of indicators (value is NaN, row sees key)
+                // marks the outputs that are NaN.
                 uint32_t any = 0;
 #pragma unroll
                 for (uint32_t j = 0; j < 4; ++j)
 #pragma unroll
                     for (uint32_t i = 0; i < C::kVBytes / 4; ++i) any |= e4m3_nan_flags(vw[j][i]);
                 if (__any_sync(0xFFFFFFFFu, any != 0u)) {
-                    uint32_t seen[4];
+                    uint32_t seen[NR][2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int k0 = key + 8 * j + 2 * static_cast<int>(c);
-                            seen[2 * j + r] = pack2<true>(k0 < row_end[r] ? 1.f : 0.f, k0 + 1 < row_end[r] ? 1.f : 0.f);
-                        }
+                        for (int k = 0; k < 2; ++k)
+                            seen[t][k] = transpose8x8(pack2<true>(key + 8 * k + static_cast<int>(g) < row_end[t][0] ? 1.f : 0.f,
+                                                                  key + 8 * k + static_cast<int>(g) < row_end[t][1] ? 1.f : 0.f));
 #pragma unroll
                     for (uint32_t i = 0; i < C::kVBytes / 4; ++i) {
                         uint32_t ind[4];
 #pragma unroll
                         for (uint32_t j = 0; j < 4; ++j) {
-                            const uint32_t full = (e4m3_nan_flags(vw[j][i]) >> 7) * 0xFFu;   // 0xFF where NaN
-                            ind[j] = full & 0x38383838u;                                     // E4M3 1.0
-                            vw[j][i] &= ~full;
+                            const uint32_t nan = (e4m3_nan_flags(vw[j][i]) >> 7) * 0xFFu;   // 0xFF where NaN
+                            ind[j] = nan & 0x38383838u;                                     // E4M3 1.0
+                            vw[j][i] &= ~nan;
                         }
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint32_t sel = half ? 0x7362u : 0x5140u;
-                            uint32_t a0, a1, c0, c1;
-                            e4m3x4_to_f16x4(prmt(ind[0], ind[1], sel), a0, a1);
-                            e4m3x4_to_f16x4(prmt(ind[2], ind[3], sel), c0, c1);
-                            float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(t0, seen, a0, c0);
-                            mma_f16(t1, seen, a1, c1);
+                            uint32_t a[4];
+                            e4m3x4_to_f16x4(prmt(ind[0], ind[1], sel), a[0], a[1]);
+                            e4m3x4_to_f16x4(prmt(ind[2], ind[3], sel), a[2], a[3]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (t0[e] > 0.f) o[4 * i + 2 * half][e] = __uint_as_float(0x7FC00000u);
-                                if (t1[e] > 0.f) o[4 * i + 2 * half + 1][e] = __uint_as_float(0x7FC00000u);
+                            for (uint32_t t = 0; t < NR; ++t) {
+                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(hit, a, seen[t][0], seen[t][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (hit[e] > 0.f) o[t][2 * i + half][e] = __uint_as_float(0x7FC00000u);
                             }
                         }
                     }
@@ -472,43 +483,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t sel = half ? 0x7362u : 0x5140u;   // (key, key + 1) byte pairs of two dims
-                    uint32_t a0, a1, c0, c1;
-                    e4m3x4_to_f16x4(prmt(vw[0][i], vw[1][i], sel), a0, a1);
-                    e4m3x4_to_f16x4(prmt(vw[2][i], vw[3][i], sel), c0, c1);
-                    mma_f16(o[4 * i + 2 * half], pf, a0, c0);
-                    mma_f16(o[4 * i + 2 * half + 1], pf, a1, c1);
+                    uint32_t a[4];
+                    e4m3x4_to_f16x4(prmt(vw[0][i], vw[1][i], sel), a[0], a[1]);
+                    e4m3x4_to_f16x4(prmt(vw[2][i], vw[3][i], sel), a[2], a[3]);
+#pragma unroll
+                    for (uint32_t t = 0; t < NR; ++t) mma_f16(o[t][2 * i + half], a, pb[t][0], pb[t][1]);
                 }
         }
-        cp_async_wait_group<0>();
+        taken += nsteps;
 
-        // ---- join the warps' parts. Output column n of tile 4 i + e holds dim
-        // n * kVPiece + (4 i + e) % kVPiece of piece (4 i + e) / kVPiece (8 kVPiece dims each).
+        // ---- join the warps' parts. Word i of a value row piece holds dims 4 i .. 4 i + 3 of it: tile
+        // 2 i + half, elements e and 2 + e are dims 4 i + 2 half and + 1 of row 2 c + e.
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-            if (c == 0) {
-                sh_m[warp][g + 8 * r] = m[r];
-                sh_l[warp][g + 8 * r] = l[r];
+        for (uint32_t t = 0; t < NR; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], 4);
+                l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], 8);
+                l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], 16);
+                if (g == 0) {
+                    sh_m[warp][8 * t + 2 * c + e] = m[t][e];
+                    sh_l[warp][8 * t + 2 * c + e] = l[t][e];
+                }
             }
-        }
         __syncwarp();   // every lane is done with its ring slots, which `merge` reuses
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (uint32_t t = 0; t < NR; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (uint32_t i = 0; i < C::kVPieces; ++i)
-#pragma unroll
-                    for (uint32_t k = 0; k < C::kVPiece; k += 4)
-                        *reinterpret_cast<float4*>(merge + (g + 8 * r) * DP + i * 8 * C::kVPiece + (2 * c + e) * C::kVPiece + k) =
-                            make_float4(o[i * C::kVPiece + k][2 * r + e], o[i * C::kVPiece + k + 1][2 * r + e],
-                                        o[i * C::kVPiece + k + 2][2 * r + e], o[i * C::kVPiece + k + 3][2 * r + e]);
+                for (uint32_t i = 0; i < C::kVBytes / 4; ++i) {
+                    const uint32_t d = (4 * i / C::kVPiece) * 8 * C::kVPiece + g * C::kVPiece + 4 * i % C::kVPiece;
+                    *reinterpret_cast<float4*>(merge + (8 * t + 2 * c + e) * DP + d) =
+                        make_float4(o[t][2 * i][e], o[t][2 * i][2 + e], o[t][2 * i + 1][e], o[t][2 * i + 1][2 + e]);
+                }
         __syncthreads();
         const bool whole = nunits == it.units;
         if (first_part && threadIdx.x == 0) write_boundary(p.ws, u, u - unit0, it.units, seq, h, item % it.tiles, total, ctas);
-        float* slot_ws = slots + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * slot_floats(DP);
-        for (uint32_t i = threadIdx.x; i < kRows * DP / 4; i += kThreads) {
+        float* const slot_ws = slots + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * slot_floats(DP);
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < C::kRows * DP / 4; i += kThreads) {
             const uint32_t r = i / (DP / 4), d = (i % (DP / 4)) * 4;
             if (row0 + r >= nrows || d >= D) continue;
             float mm = sh_m[0][r];
@@ -535,11 +549,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) kv_attn_kernel(
             } else {
                 *reinterpret_cast<float4*>(slot_ws + r * DP + d) = acc;
                 if (d == 0) {
-                    slot_ws[kRows * DP + r] = mm;
-                    slot_ws[kRows * DP + kRows + r] = ll;
+                    slot_ws[kMaxRows * DP + r] = mm;
+                    slot_ws[kMaxRows * DP + kMaxRows + r] = ll;
                 }
             }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();   // the rings and sh_* are free again
         first_part = false;
         u += nunits;
@@ -554,12 +569,12 @@ __global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p
     grid_launch_dependents();
     const uint32_t c = blockIdx.x + 1, lane = threadIdx.x & 31, r = blockIdx.y * kWarps + (threadIdx.x >> 5);
     const Boundary b = reinterpret_cast<const Boundary*>(p.ws)[c];
-    const uint32_t row = b.tile * kRows + r;
+    const uint32_t row = b.tile * p.tile_rows + r;
     if (b.parts == 0 || row >= static_cast<uint32_t>(b.count) * p.group) return;
     const float* const slots = p.ws + boundary_floats(p.ctas);
     const auto slot = [&](uint32_t i) { return slots + static_cast<uint64_t>(i == 0 ? b.slot : 2 * (c + i - 1)) * slot_floats(DP); };
     float m = -INFINITY;
-    for (uint32_t i = lane; i < b.parts; i += 32) m = fmaxf(m, slot(i)[kRows * DP + r]);
+    for (uint32_t i = lane; i < b.parts; i += 32) m = fmaxf(m, slot(i)[kMaxRows * DP + r]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     constexpr uint32_t V = DP / 32;   // consecutive dims of a lane
@@ -567,9 +582,9 @@ __global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p
 #pragma unroll 8
     for (uint32_t i = 0; i < b.parts; ++i) {
         const float* s = slot(i);
-        const float mi = s[kRows * DP + r];
+        const float mi = s[kMaxRows * DP + r];
         const float a = mi == -INFINITY ? 0.f : ex2(mi - m);
-        l = fmaf(a, s[kRows * DP + kRows + r], l);
+        l = fmaf(a, s[kMaxRows * DP + kMaxRows + r], l);
         float x[V];
         if constexpr (V == 2) {
             const float2 t = *reinterpret_cast<const float2*>(s + r * DP + 2 * lane);
@@ -592,53 +607,58 @@ __global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p
         if (V * lane + k < p.c.head_dim) *reinterpret_cast<uint32_t*>(dst + V * lane + k) = pack2<F16>(acc[k] * inv, acc[k + 1] * inv);
 }
 
-template <bool F16, uint32_t DP>
-cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<F16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+template <bool F16, uint32_t DP, uint32_t NR>
+cudaError_t launch(AttnArgs p, int sms, cudaStream_t s) {
+    using C = Cfg<DP, NR>;
+    p.tile_rows = C::kRows;
+    p.ctas = static_cast<uint32_t>(sms) * C::kCtasPerSm;
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<F16, DP, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(p.ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<F16, DP>, p);
-    if (e != cudaSuccess) return e;
-    if (p.ctas < 2) return cudaSuccess;
+    e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<F16, DP, NR>, p);
+    if (e != cudaSuccess || p.ctas < 2) return e;
     const uint64_t rows = static_cast<uint64_t>(p.b.max_q) * p.group;   // of an item, at most
-    cfg.gridDim = dim3(p.ctas - 1, (static_cast<uint32_t>(rows < kRows ? rows : kRows) + kWarps - 1) / kWarps, 1);
+    cfg.gridDim = dim3(p.ctas - 1, (static_cast<uint32_t>(rows < C::kRows ? rows : C::kRows) + kWarps - 1) / kWarps, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<F16, DP>, p);
 }
-
-uint32_t padded_dim(uint32_t d) { return d <= 64 ? 64u : d <= 128 ? 128u : 256u; }
-uint32_t grid_ctas(uint32_t dp, int sms) { return static_cast<uint32_t>(sms) * (dp == 256 ? Cfg<256>::kCtasPerSm : Cfg<128>::kCtasPerSm); }
+template <bool F16, uint32_t DP>
+cudaError_t launch_rows(const AttnArgs& p, int sms, cudaStream_t s) {
+    return p.b.max_q * static_cast<uint64_t>(p.group) <= 8 ? launch<F16, DP, 1>(p, sms, s) : launch<F16, DP, 2>(p, sms, s);
+}
+template <bool F16>
+cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t s) {
+    return p.c.head_dim <= 64 ? launch_rows<F16, 64>(p, sms, s) : p.c.head_dim <= 128 ? launch_rows<F16, 128>(p, sms, s) : launch_rows<F16, 256>(p, sms, s);
+}
 
 }  // namespace
 
 uint64_t kv_attn_ws_bytes(uint32_t head_dim, uint32_t rows_per_head, int sms) {
     if (kv_attn_tc_applies(head_dim, rows_per_head)) return kv_attn_tc_ws_bytes(head_dim, sms);
-    const uint32_t dp = padded_dim(head_dim);
-    return 4 * boundary_floats(grid_ctas(dp, sms)) + 8ull * grid_ctas(dp, sms) * slot_floats(dp);
+    const uint32_t ctas = static_cast<uint32_t>(sms) * kMostCtasPerSm, dp = head_dim <= 64 ? 64u : head_dim <= 128 ? 128u : 256u;
+    return 4 * boundary_floats(ctas) + 8ull * ctas * slot_floats(dp);
 }
 
 int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& q,
-                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms,
-                   uint64_t timeout_ns, cudaStream_t s, std::string* err) {
-    AttnArgs p{c, b, q, out, static_cast<float*>(ws), softmax_scale * 1.4426950408889634f, q.heads / c.kv_heads, 0, 0, timeout_ns};
+                   const w8a16_heads_t& out, float softmax_scale, void* ws, int sms, uint64_t timeout_ns, cudaStream_t s,
+                   std::string* err) {
+    AttnArgs p{c, b, q, out, static_cast<float*>(ws), softmax_scale * 1.4426950408889634f, q.heads / c.kv_heads, 0, 0, 0, timeout_ns};
     while ((1u << p.page_shift) < c.page_size) ++p.page_shift;
-    const uint32_t dp = padded_dim(c.head_dim);
-    p.ctas = grid_ctas(dp, sms);
     const bool f16 = act_dtype == W8A16_ACT_F16;
-    const cudaError_t e = kv_attn_tc_applies(c.head_dim, b.max_q * p.group) ? launch_kv_attn_tc(p, f16, sms, s)
-                          : dp == 64    ? (f16 ? launch<true, 64>(p, s) : launch<false, 64>(p, s))
-                          : dp == 128 ? (f16 ? launch<true, 128>(p, s) : launch<false, 128>(p, s))
-                                      : (f16 ? launch<true, 256>(p, s) : launch<false, 256>(p, s));
+    const uint64_t rows = static_cast<uint64_t>(b.max_q) * p.group;
+    const cudaError_t e = kv_attn_tc_applies(c.head_dim, static_cast<uint32_t>(rows < 0x7FFFFFFFu ? rows : 0x7FFFFFFFu))
+                              ? launch_kv_attn_tc(p, f16, sms, s)
+                              : f16 ? launch_dim<true>(p, sms, s) : launch_dim<false>(p, sms, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         *err = std::string("cache attention launch failed: ") + cudaGetErrorString(e);

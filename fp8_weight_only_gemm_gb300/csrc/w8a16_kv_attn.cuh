@@ -14,6 +14,7 @@ struct AttnArgs {
     uint32_t group;         // query heads per key/value head
     uint32_t page_shift;
     uint32_t ctas;          // of the attention kernel
+    uint32_t tile_rows;     // query rows of an item (the kernel for few rows)
     uint64_t timeout_ns;    // limit of an in-kernel wait
 };
 
