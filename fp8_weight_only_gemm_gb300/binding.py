@@ -543,30 +543,32 @@ def quantize_weights_ptr(W_ptr, w_dtype, w_row_stride, N, K, codes_ptr, scale_pt
 
 
 # ------------------------------------------------- 8-bit paged key/value cache --
+# These calls are short (a decode step's append runs for some 3 us), so what is asked of a
+# tensor is asked once: the checks below are as few Python operations as they can be.
 def _act_type(t, name) -> int:
     import torch
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return ACT_BF16
-    if t.dtype is torch.float16:
+    if dtype is torch.float16:
         return ACT_F16
-    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
 
 
 def _device_call(index, stream, fn, *args):
     """fn(*args, stream handle) on CUDA device `index` (stream None: its current one)."""
     import torch
-    if index == torch.cuda.current_device():
-        if stream is None:
-            return fn(*args, torch._C._cuda_getCurrentRawStream(index))
-        return fn(*args, _stream_handle(stream))
-    with torch.cuda.device(index):
-        return fn(*args, _stream_handle(stream))
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream_handle(stream))
+    if rc:
+        _check(rc)
 
 
-def _same_gpu(index, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"all tensors must be on one CUDA device (cuda:{index}; got {t.device})")
+def _off_device(index, t):
+    return ValueError(f"all tensors must be on one CUDA device (cuda:{index}; got {t.device})")
 
 
 class KVCache:
@@ -613,33 +615,44 @@ class KVCache:
 
 def _kv_batch(cache, rows, page_table, lens, cu_q, max_q) -> KvBatchDesc:
     import torch
-    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.stride(1) != 1:
+    int32, index = torch.int32, cache._index
+    shape, strides = page_table.shape, page_table.stride()
+    if len(shape) != 2 or strides[1] != 1 or page_table.dtype is not int32:
         raise ValueError("page_table must be int32 [batch, max_pages] with contiguous rows")
-    B, max_pages = page_table.shape
-    if lens.dtype is not torch.int32 or lens.dim() != 1 or lens.shape[0] != B or not lens.is_contiguous():
+    B, max_pages = shape
+    if lens.shape != (B,) or lens.dtype is not int32 or not lens.is_contiguous():
         raise ValueError(f"lens must be contiguous int32 [{B}]")
+    if page_table.get_device() != index:
+        raise _off_device(index, page_table)
+    if lens.get_device() != index:
+        raise _off_device(index, lens)
+    cu = None
     if cu_q is None:
         if max_q is None:
             if B == 0 or rows % B:
                 raise ValueError(f"{rows} rows do not divide among {B} sequences: pass cu_q and max_q")
             max_q = rows // B
     else:
-        if cu_q.dtype is not torch.int32 or cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
+        if cu_q.shape != (B + 1,) or cu_q.dtype is not int32 or not cu_q.is_contiguous():
             raise ValueError(f"cu_q must be contiguous int32 [{B + 1}]")
+        if cu_q.get_device() != index:
+            raise _off_device(index, cu_q)
         if max_q is None:
             raise ValueError("cu_q needs max_q, the most rows of one sequence")
-    _same_gpu(cache._index, page_table, lens, cu_q)
-    return KvBatchDesc(page_table.data_ptr(), lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(),
-                       page_table.stride(0), max_pages, B, rows, max_q)
+        cu = cu_q.data_ptr()
+    return KvBatchDesc(page_table.data_ptr(), lens.data_ptr(), cu, strides[0], max_pages, B, rows, max_q)
 
 
 def _heads(cache, t, name, rows, dtype) -> HeadsDesc:
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[2] != cache.head_dim or strides[2] != 1:
         raise ValueError(f"{name} must be [{rows}, heads, {cache.head_dim}] with unit stride along the head; "
-                         f"got {list(t.shape)}")
+                         f"got {list(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like the others, got {t.dtype}")
-    return HeadsDesc(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+    if t.get_device() != cache._index:
+        raise _off_device(cache._index, t)
+    return HeadsDesc(t.data_ptr(), strides[0], strides[1], shape[1])
 
 
 def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_out=None, cu_q=None, max_q=None,
@@ -655,33 +668,38 @@ def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_ou
     cu_q (int32 [batch + 1] offsets) with max_q the most rows of one. cos, sin: float32
     [positions, rotary_dim / 2], rotary_dim a multiple of 16 up to head_dim (None: no
     rotation); pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved."""
-    import torch
-    rows = k.shape[0]
-    act = _act_type(k, "k")
+    rows, dtype, act = k.shape[0], k.dtype, _act_type(k, "k")
     batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
-    kd, vd = _heads(cache, k, "k", rows, k.dtype), _heads(cache, v, "v", rows, k.dtype)
+    kd, vd = _heads(cache, k, "k", rows, dtype), _heads(cache, v, "v", rows, dtype)
     qd = od = None
     if q is not None:
-        qd = _heads(cache, q, "q", rows, k.dtype)
+        qd = _heads(cache, q, "q", rows, dtype)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        od = _heads(cache, q_out, "q_out", rows, k.dtype)
-        qd_ref, od_ref = ctypes.byref(qd), ctypes.byref(od)
-    else:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        qd_ref = od_ref = None
+            import torch
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        od = _heads(cache, q_out, "q_out", rows, dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     if cos is None:
-        rope = RopeDesc(None, None, 0, 0, 0)
+        rope = _NO_ROPE
     else:
-        if (sin is None or cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not torch.float32
-                or sin.dtype is not torch.float32 or not cos.is_contiguous() or not sin.is_contiguous()):
-            raise ValueError("cos and sin must be contiguous float32 [positions, rotary_dim / 2]")
-        rope = RopeDesc(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], 1 if interleaved else 0)
-    _same_gpu(cache._index, k, v, q, q_out, cos, sin)
-    _check(_device_call(cache._index, stream, load().w8a16_kv_append, cache._ref, ctypes.byref(batch), act,
-                        ctypes.byref(kd), ctypes.byref(vd), qd_ref, od_ref, ctypes.byref(rope)))
+        rope = _rope(cache._index, cos, sin, interleaved)
+    _device_call(cache._index, stream, load().w8a16_kv_append, cache._ref, batch, act, kd, vd, qd, od, rope)
     return q_out
+
+
+_NO_ROPE = RopeDesc(None, None, 0, 0, 0)
+
+
+def _rope(index, cos, sin, interleaved) -> RopeDesc:
+    import torch
+    shape, f32 = cos.shape, torch.float32
+    if (sin is None or len(shape) != 2 or sin.shape != shape or cos.dtype is not f32 or sin.dtype is not f32
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        raise ValueError("cos and sin must be contiguous float32 [positions, rotary_dim / 2]")
+    if cos.get_device() != index or sin.get_device() != index:
+        raise _off_device(index, cos)
+    return RopeDesc(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if interleaved else 0)
 
 
 def kv_attention_workspace_bytes(cache, batch, max_q, heads) -> int:
@@ -704,22 +722,22 @@ def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu
     kv_attention_workspace_bytes(...) bytes that no concurrent call uses (None allocates
     one for this call). Returns out, [tokens, heads, head_dim] of q's dtype."""
     import torch
-    rows = q.shape[0]
-    act = _act_type(q, "q")
+    rows, dtype, act = q.shape[0], q.dtype, _act_type(q, "q")
     batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    qd, od = _heads(cache, q, "q", rows, q.dtype), _heads(cache, out, "out", rows, q.dtype)
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    qd, od = _heads(cache, q, "q", rows, dtype), _heads(cache, out, "out", rows, dtype)
     if workspace is None:
         workspace = torch.empty(kv_attention_workspace_bytes(cache, batch.batch, batch.max_q, qd.heads),
                                 dtype=torch.uint8, device=q.device)
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    _same_gpu(cache._index, q, out, workspace)
-    if softmax_scale is None:
-        softmax_scale = cache.head_dim ** -0.5
-    _check(_device_call(cache._index, stream, load().w8a16_kv_attention, cache._ref, ctypes.byref(batch), act,
-                        ctypes.byref(qd), ctypes.byref(od), softmax_scale, workspace.data_ptr(), workspace.numel()))
+    index = cache._index
+    if workspace.get_device() != index:
+        raise _off_device(index, workspace)
+    _device_call(index, stream, load().w8a16_kv_attention, cache._ref, batch, act, qd, od,
+                 cache.head_dim ** -0.5 if softmax_scale is None else softmax_scale, workspace.data_ptr(),
+                 workspace.numel())
     return out
 
 
@@ -731,31 +749,39 @@ def gemm_w4(A, W, scale, C=None, *, zeros=None, stream=None, flags: int = 0):
     dtype, [N, K/group] with group 32, 64 or 128 (taken from its shape); zeros: uint8
     [N, K/group], 0..15 (None: 8); C: optional [M, >=N] of A's dtype."""
     import torch
-    act = _act_type(A, "A")
+    act, dtype, index = _act_type(A, "A"), A.dtype, A.get_device()
     if A.dim() != 2 or A.stride(1) != 1:
         raise ValueError("A must be [M, K] with contiguous rows")
     M, K = A.shape
-    if W.dim() != 2 or W.dtype is not torch.uint8 or not W.is_contiguous() or W.shape[1] * 2 != K:
+    wshape, sshape = W.shape, scale.shape
+    if len(wshape) != 2 or wshape[1] * 2 != K or W.dtype is not torch.uint8 or not W.is_contiguous():
         raise ValueError(f"W must be contiguous uint8 [N, {K // 2}] (two codes a byte)")
-    N = W.shape[0]
-    if scale.dim() != 2 or scale.shape[0] != N or not scale.is_contiguous() or scale.shape[1] < 1 or K % scale.shape[1]:
-        raise ValueError(f"scale must be contiguous [{N}, K/group]; got {list(scale.shape)} for K={K}")
-    if scale.dtype is not torch.float32 and scale.dtype is not A.dtype:
-        raise TypeError(f"scale must be float32 or {A.dtype}, got {scale.dtype}")
-    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != scale.shape or not zeros.is_contiguous()):
-        raise ValueError(f"zeros must be contiguous uint8 {list(scale.shape)}")
+    N = wshape[0]
+    if len(sshape) != 2 or sshape[0] != N or sshape[1] < 1 or K % sshape[1] or not scale.is_contiguous():
+        raise ValueError(f"scale must be contiguous [{N}, K/group]; got {list(sshape)} for K={K}")
+    if scale.dtype is torch.float32:
+        scale_type = 0
+    elif scale.dtype is dtype:
+        scale_type = 1
+    else:
+        raise TypeError(f"scale must be float32 or {dtype}, got {scale.dtype}")
+    z = None
+    if zeros is not None:
+        if zeros.shape != sshape or zeros.dtype is not torch.uint8 or not zeros.is_contiguous():
+            raise ValueError(f"zeros must be contiguous uint8 {list(sshape)}")
+        if zeros.get_device() != index:
+            raise _off_device(index, zeros)
+        z = zeros.data_ptr()
     if C is None:
-        C = torch.empty((M, N), dtype=A.dtype, device=A.device)
-    elif C.dtype is not A.dtype or C.dim() != 2 or C.stride(1) != 1 or C.shape[0] != M or C.shape[1] < N:
-        raise ValueError(f"C must be {A.dtype} [{M}, >={N}] with contiguous rows")
-    index = A.get_device()
+        C = torch.empty((M, N), dtype=dtype, device=A.device)
+    elif C.dtype is not dtype or C.dim() != 2 or C.stride(1) != 1 or C.shape[0] != M or C.shape[1] < N:
+        raise ValueError(f"C must be {dtype} [{M}, >={N}] with contiguous rows")
     if index < 0:
         raise ValueError("all tensors must be on a CUDA device")
-    _same_gpu(index, W, scale, zeros, C)
-    _check(_device_call(index, stream, load().w8a16_gemm_w4, A.data_ptr(), A.stride(0), act, W.data_ptr(),
-                        scale.data_ptr(), 0 if scale.dtype is torch.float32 else 1,
-                        None if zeros is None else zeros.data_ptr(), K // scale.shape[1], C.data_ptr(), C.stride(0),
-                        M, N, K, flags))
+    if W.get_device() != index or scale.get_device() != index or C.get_device() != index:
+        raise _off_device(index, W)
+    _device_call(index, stream, load().w8a16_gemm_w4, A.data_ptr(), A.stride(0), act, W.data_ptr(), scale.data_ptr(),
+                 scale_type, z, K // sshape[1], C.data_ptr(), C.stride(0), M, N, K, flags)
     return C
 
 
