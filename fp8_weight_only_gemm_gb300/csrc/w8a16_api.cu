@@ -1269,19 +1269,22 @@ int w8a16_device_status(w8a16_stream_t stream, int clear, uint32_t* status, uint
         e = w8a16::w8a8_status_read(&wa, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess)
         e = w8a16::gemv_status_read(&wg, clear != 0, reinterpret_cast<cudaStream_t>(stream));
-    w8a16::StatusWord wk{0, 0, 0}, wt{0, 0, 0}, wp{0, 0, 0};
+    w8a16::StatusWord wk{0, 0, 0}, wt{0, 0, 0}, wp{0, 0, 0}, w4{0, 0, 0};
     if (e == cudaSuccess)
         e = w8a16::kv_append_status_read(&wk, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess)
         e = w8a16::kv_attn_status_read(&wt, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess)
         e = w8a16::kv_attn_tc_status_read(&wp, clear != 0, reinterpret_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess)
+        e = w8a16::w4_status_read(&w4, clear != 0, reinterpret_cast<cudaStream_t>(stream));
     if (w.code == 0) w = w8;
     if (w.code == 0) w = wa;
     if (w.code == 0) w = wg;
     if (w.code == 0) w = wk;
     if (w.code == 0) w = wt;
     if (w.code == 0) w = wp;
+    if (w.code == 0) w = w4;
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(W8A16_ERR_DEVICE, std::string("w8a16_device_status: ") + cudaGetErrorString(e));

@@ -217,10 +217,13 @@ int w8a16_gemm_w4(const void* A, uint32_t a_row_stride, uint32_t act_dtype, cons
         int sms = 0;
         rc = w8a16::api_device(&sms);
         if (rc) return rc;
+        uint64_t timeout_ns = 0;
+        rc = w8a16::api_timeout(&timeout_ns);
+        if (rc) return rc;
         std::string err;
         rc = w8a16::launch_w4({A, W, scale, zeros, C, a_row_stride, c_row_stride, M, N, K, group, act_dtype,
                                scale_dtype == W8A16_W4_SCALE_F32},
-                              sms, flags, reinterpret_cast<cudaStream_t>(stream), &err);
+                              sms, timeout_ns, flags, reinterpret_cast<cudaStream_t>(stream), &err);
         return rc ? api_fail(rc, err) : api_ok();
     });
 }

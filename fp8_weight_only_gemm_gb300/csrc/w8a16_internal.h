@@ -296,7 +296,8 @@ struct W4Operands {
     uint32_t lda, ldc, M, N, K, group, act_dtype;
     bool scale_f32;
 };
-int launch_w4(const W4Operands& o, int sms, uint32_t flags, cudaStream_t s, std::string* err);
+int launch_w4(const W4Operands& o, int sms, uint64_t timeout_ns, uint32_t flags, cudaStream_t s, std::string* err);
+cudaError_t w4_status_read(StatusWord* out, bool clear, cudaStream_t s);
 
 // Shared by the C entries of every translation unit (w8a16_api.cu): the last error's
 // message of this host thread, and the current device (sm_103 or an error).
@@ -308,6 +309,10 @@ int api_timeout(uint64_t* ns);   // the limit of in-kernel waits (W8A16_WAIT_TIM
 // TMA descriptors of W ([N][K] E4M3, 128x128 boxes) and A ([M][K] BF16 at the
 // caller's pitch, 64 x token_tile boxes), 128-byte swizzle; cached per device.
 bool tc_tensor_map_w(const GemmArgs& g, int device, CUtensorMap* out, std::string* err);
+// A descriptor of a row-major matrix of 1- or 2-byte elements, encoded at every call: boxes
+// of 64- or 128-byte rows with the swizzle of that size, zeros outside the matrix.
+bool tensor_map_2d(const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride_bytes, uint32_t elem_bytes,
+                   uint32_t box_rows, uint32_t box_cols, CUtensorMap* out, std::string* err);
 bool tc_tensor_map_a(const GemmArgs& g, uint32_t token_tile, int device, CUtensorMap* out,
                      std::string* err);
 

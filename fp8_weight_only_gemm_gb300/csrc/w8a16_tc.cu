@@ -681,6 +681,25 @@ int launch_tc(const GemmArgs& g, const w8a16_plan_t& p, cudaStream_t s, uint64_t
     return W8A16_OK;
 }
 
+bool tensor_map_2d(const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride_bytes, uint32_t elem_bytes,
+                   uint32_t box_rows, uint32_t box_cols, CUtensorMap* out, std::string* err) {
+    auto enc = encode_fn();
+    if (!enc) {
+        *err = "cuTensorMapEncodeTiled is not available from the CUDA driver";
+        return false;
+    }
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {stride_bytes};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(out, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                           const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           box_cols * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) *err = "cuTensorMapEncodeTiled failed (CUresult " + std::to_string(static_cast<int>(r)) + ")";
+    return r == CUDA_SUCCESS;
+}
+
 bool tc_tensor_map_w(const GemmArgs& g, int device, CUtensorMap* out, std::string* err) {
     return get_map({reinterpret_cast<uint64_t>(g.W), g.N, g.K, g.K, kTcRows, 0}, device, out, err);
 }
