@@ -13,6 +13,7 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "_build" / "libw8a16.so"
+MARSHAL_PATH = PKG / "_build" / "w8a16_marshal.so"
 HEADER = PKG.parent / "include" / "w8a16.h"
 
 # Values mirrored from include/w8a16.h (checked against the header by the tests).
@@ -543,32 +544,28 @@ def quantize_weights_ptr(W_ptr, w_dtype, w_row_stride, N, K, codes_ptr, scale_pt
 
 
 # ------------------------------------------------- 8-bit paged key/value cache --
-# These calls are short (a decode step's append runs for some 3 us), so what is asked of a
-# tensor is asked once: the checks below are as few Python operations as they can be.
-def _act_type(t, name) -> int:
-    import torch
-    dtype = t.dtype
-    if dtype is torch.bfloat16:
-        return ACT_BF16
-    if dtype is torch.float16:
-        return ACT_F16
-    raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
+# These calls are short (a decode step's append runs for some 3 us). What they ask of their
+# tensors, and the checks that only tensors allow, is in csrc/w8a16_marshal.cpp.
+_marshal = None
 
 
-def _device_call(index, stream, fn, *args):
-    """fn(*args, stream handle) on CUDA device `index` (stream None: its current one)."""
-    import torch
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _stream_handle(stream))
-    if rc:
-        _check(rc)
+def _load_marshal():
+    global _marshal
+    import importlib.machinery
+    import importlib.util
 
-
-def _off_device(index, t):
-    return ValueError(f"all tensors must be on one CUDA device (cuda:{index}; got {t.device})")
+    import torch  # noqa: F401  the module resolves torch's libraries, which this loads
+    lib = load()
+    if not MARSHAL_PATH.exists():
+        raise RuntimeError(f"{MARSHAL_PATH} is missing: build it first (python -m fp8_weight_only_gemm_gb300.build "
+                           "or __graft_entry__.build()); there is no fallback path")
+    loader = importlib.machinery.ExtensionFileLoader("w8a16_marshal", str(MARSHAL_PATH))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("w8a16_marshal", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
+                  for fn in (lib.w8a16_kv_append, lib.w8a16_kv_attention, lib.w8a16_gemm_w4)))
+    _marshal = module
+    return module
 
 
 class KVCache:
@@ -602,6 +599,7 @@ class KVCache:
             k_codes.stride(0), k_codes.stride(1), k_codes.stride(2), k_scale.stride(0), k_scale.stride(1),
             self.num_pages, self.page_size, self.kv_heads, self.head_dim)
         self._ref = ctypes.byref(self._desc)
+        self._address = ctypes.addressof(self._desc)
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, device="cuda"):
@@ -611,48 +609,6 @@ class KVCache:
               for _ in range(2)]
         sc = [torch.zeros(num_pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2)]
         return cls(*kv, *sc)
-
-
-def _kv_batch(cache, rows, page_table, lens, cu_q, max_q) -> KvBatchDesc:
-    import torch
-    int32, index = torch.int32, cache._index
-    shape, strides = page_table.shape, page_table.stride()
-    if len(shape) != 2 or strides[1] != 1 or page_table.dtype is not int32:
-        raise ValueError("page_table must be int32 [batch, max_pages] with contiguous rows")
-    B, max_pages = shape
-    if lens.shape != (B,) or lens.dtype is not int32 or not lens.is_contiguous():
-        raise ValueError(f"lens must be contiguous int32 [{B}]")
-    if page_table.get_device() != index:
-        raise _off_device(index, page_table)
-    if lens.get_device() != index:
-        raise _off_device(index, lens)
-    cu = None
-    if cu_q is None:
-        if max_q is None:
-            if B == 0 or rows % B:
-                raise ValueError(f"{rows} rows do not divide among {B} sequences: pass cu_q and max_q")
-            max_q = rows // B
-    else:
-        if cu_q.shape != (B + 1,) or cu_q.dtype is not int32 or not cu_q.is_contiguous():
-            raise ValueError(f"cu_q must be contiguous int32 [{B + 1}]")
-        if cu_q.get_device() != index:
-            raise _off_device(index, cu_q)
-        if max_q is None:
-            raise ValueError("cu_q needs max_q, the most rows of one sequence")
-        cu = cu_q.data_ptr()
-    return KvBatchDesc(page_table.data_ptr(), lens.data_ptr(), cu, strides[0], max_pages, B, rows, max_q)
-
-
-def _heads(cache, t, name, rows, dtype) -> HeadsDesc:
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != rows or shape[2] != cache.head_dim or strides[2] != 1:
-        raise ValueError(f"{name} must be [{rows}, heads, {cache.head_dim}] with unit stride along the head; "
-                         f"got {list(shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype} like the others, got {t.dtype}")
-    if t.get_device() != cache._index:
-        raise _off_device(cache._index, t)
-    return HeadsDesc(t.data_ptr(), strides[0], strides[1], shape[1])
 
 
 def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_out=None, cu_q=None, max_q=None,
@@ -668,38 +624,18 @@ def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_ou
     cu_q (int32 [batch + 1] offsets) with max_q the most rows of one. cos, sin: float32
     [positions, rotary_dim / 2], rotary_dim a multiple of 16 up to head_dim (None: no
     rotation); pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved."""
-    rows, dtype, act = k.shape[0], k.dtype, _act_type(k, "k")
-    batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
-    kd, vd = _heads(cache, k, "k", rows, dtype), _heads(cache, v, "v", rows, dtype)
-    qd = od = None
-    if q is not None:
-        qd = _heads(cache, q, "q", rows, dtype)
-        if q_out is None:
-            import torch
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        od = _heads(cache, q_out, "q_out", rows, dtype)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if cos is None:
-        rope = _NO_ROPE
-    else:
-        rope = _rope(cache._index, cos, sin, interleaved)
-    _device_call(cache._index, stream, load().w8a16_kv_append, cache._ref, batch, act, kd, vd, qd, od, rope)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    elif q_out is None:
+        import torch
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rc = (_marshal or _load_marshal()).kv_append(
+        cache._address, cache._index, cache.head_dim, k, v, page_table, lens, cu_q, max_q, q, q_out, cos, sin,
+        interleaved, stream if stream is None else _stream_handle(stream))
+    if rc:
+        _check(rc)
     return q_out
-
-
-_NO_ROPE = RopeDesc(None, None, 0, 0, 0)
-
-
-def _rope(index, cos, sin, interleaved) -> RopeDesc:
-    import torch
-    shape, f32 = cos.shape, torch.float32
-    if (sin is None or len(shape) != 2 or sin.shape != shape or cos.dtype is not f32 or sin.dtype is not f32
-            or not cos.is_contiguous() or not sin.is_contiguous()):
-        raise ValueError("cos and sin must be contiguous float32 [positions, rotary_dim / 2]")
-    if cos.get_device() != index or sin.get_device() != index:
-        raise _off_device(index, cos)
-    return RopeDesc(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if interleaved else 0)
 
 
 def kv_attention_workspace_bytes(cache, batch, max_q, heads) -> int:
@@ -721,23 +657,21 @@ def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu
     defaults to head_dim ** -0.5. workspace: a CUDA uint8 tensor of
     kv_attention_workspace_bytes(...) bytes that no concurrent call uses (None allocates
     one for this call). Returns out, [tokens, heads, head_dim] of q's dtype."""
-    import torch
-    rows, dtype, act = q.shape[0], q.dtype, _act_type(q, "q")
-    batch = _kv_batch(cache, rows, page_table, lens, cu_q, max_q)
-    if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    qd, od = _heads(cache, q, "q", rows, dtype), _heads(cache, out, "out", rows, dtype)
-    if workspace is None:
-        workspace = torch.empty(kv_attention_workspace_bytes(cache, batch.batch, batch.max_q, qd.heads),
-                                dtype=torch.uint8, device=q.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    index = cache._index
-    if workspace.get_device() != index:
-        raise _off_device(index, workspace)
-    _device_call(index, stream, load().w8a16_kv_attention, cache._ref, batch, act, qd, od,
-                 cache.head_dim ** -0.5 if softmax_scale is None else softmax_scale, workspace.data_ptr(),
-                 workspace.numel())
+    if out is None or workspace is None:
+        import torch
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            B = page_table.shape[0]
+            most = max_q if max_q is not None else -(-q.shape[0] // max(B, 1))
+            workspace = torch.empty(kv_attention_workspace_bytes(cache, B, most, q.shape[1]), dtype=torch.uint8,
+                                    device=q.device)
+    rc = (_marshal or _load_marshal()).kv_attention(
+        cache._address, cache._index, cache.head_dim, q, out, page_table, lens, cu_q, max_q,
+        cache.head_dim ** -0.5 if softmax_scale is None else softmax_scale, workspace,
+        stream if stream is None else _stream_handle(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -748,40 +682,13 @@ def gemm_w4(A, W, scale, C=None, *, zeros=None, stream=None, flags: int = 0):
     2j in the low half of byte j and 2j + 1 in its high half; scale: float32 or A's
     dtype, [N, K/group] with group 32, 64 or 128 (taken from its shape); zeros: uint8
     [N, K/group], 0..15 (None: 8); C: optional [M, >=N] of A's dtype."""
-    import torch
-    act, dtype, index = _act_type(A, "A"), A.dtype, A.get_device()
-    if A.dim() != 2 or A.stride(1) != 1:
-        raise ValueError("A must be [M, K] with contiguous rows")
-    M, K = A.shape
-    wshape, sshape = W.shape, scale.shape
-    if len(wshape) != 2 or wshape[1] * 2 != K or W.dtype is not torch.uint8 or not W.is_contiguous():
-        raise ValueError(f"W must be contiguous uint8 [N, {K // 2}] (two codes a byte)")
-    N = wshape[0]
-    if len(sshape) != 2 or sshape[0] != N or sshape[1] < 1 or K % sshape[1] or not scale.is_contiguous():
-        raise ValueError(f"scale must be contiguous [{N}, K/group]; got {list(sshape)} for K={K}")
-    if scale.dtype is torch.float32:
-        scale_type = 0
-    elif scale.dtype is dtype:
-        scale_type = 1
-    else:
-        raise TypeError(f"scale must be float32 or {dtype}, got {scale.dtype}")
-    z = None
-    if zeros is not None:
-        if zeros.shape != sshape or zeros.dtype is not torch.uint8 or not zeros.is_contiguous():
-            raise ValueError(f"zeros must be contiguous uint8 {list(sshape)}")
-        if zeros.get_device() != index:
-            raise _off_device(index, zeros)
-        z = zeros.data_ptr()
     if C is None:
-        C = torch.empty((M, N), dtype=dtype, device=A.device)
-    elif C.dtype is not dtype or C.dim() != 2 or C.stride(1) != 1 or C.shape[0] != M or C.shape[1] < N:
-        raise ValueError(f"C must be {dtype} [{M}, >={N}] with contiguous rows")
-    if index < 0:
-        raise ValueError("all tensors must be on a CUDA device")
-    if W.get_device() != index or scale.get_device() != index or C.get_device() != index:
-        raise _off_device(index, W)
-    _device_call(index, stream, load().w8a16_gemm_w4, A.data_ptr(), A.stride(0), act, W.data_ptr(), scale.data_ptr(),
-                 scale_type, z, K // sshape[1], C.data_ptr(), C.stride(0), M, N, K, flags)
+        import torch
+        C = torch.empty((A.shape[0], W.shape[0]), dtype=A.dtype, device=A.device)
+    rc = (_marshal or _load_marshal()).gemm_w4(A, W, scale, C, zeros, flags,
+                                               stream if stream is None else _stream_handle(stream))
+    if rc:
+        _check(rc)
     return C
 
 

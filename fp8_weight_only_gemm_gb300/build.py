@@ -2,8 +2,9 @@
 
 Usage: ``python -m fp8_weight_only_gemm_gb300.build`` or ``build_library()``.
 Each CUDA translation unit compiles in parallel to an object; one link step
-makes ``fp8_weight_only_gemm_gb300/_build/libw8a16.so``. A stamp of the
-sources' hash and the flags skips rebuilding when nothing changed.
+makes ``fp8_weight_only_gemm_gb300/_build/libw8a16.so``. Beside them g++ makes the
+binding's extension module w8a16_marshal.so from the installed torch's headers. A
+stamp of the sources' hash and the flags skips rebuilding when nothing changed.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libw8a16.so"
+MARSHAL = BUILD / "w8a16_marshal.so"
 
 SOURCES = ["w8a16_api.cu", "w8a16_simt.cu", "w8a16_tc.cu", "w8a16_tc8.cu", "w8a16_w8a8.cu",
            "w8a16_quant.cu", "w8a16_gemv.cu", "w8a16_decode_api.cu", "w8a16_kv_append.cu", "w8a16_kv_attn.cu",
@@ -35,6 +37,24 @@ def _nvcc() -> str:
         if cand and Path(cand).exists():
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is needed to build libw8a16.so")
+
+
+def _build_marshal() -> None:
+    import importlib.metadata
+    import sysconfig
+
+    torch_dir = Path(importlib.metadata.distribution("torch").locate_file("torch"))
+    cuda = Path(_nvcc()).resolve().parent.parent
+    tmp = BUILD / f"w8a16_marshal.so.tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I", str(INCLUDE), "-I", str(torch_dir / "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", str(cuda / "include"), str(CSRC / "w8a16_marshal.cpp"), "-o", str(tmp),
+           "-L", str(torch_dir / "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{torch_dir / 'lib'}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on w8a16_marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def _stamp() -> str:
@@ -52,7 +72,7 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
     BUILD.mkdir(parents=True, exist_ok=True)
     stamp_file = BUILD / "stamp"
     stamp = _stamp()
-    if not force and LIB.exists() and stamp_file.exists() and stamp_file.read_text() == stamp:
+    if not force and LIB.exists() and MARSHAL.exists() and stamp_file.exists() and stamp_file.read_text() == stamp:
         return LIB
     nvcc = _nvcc()
     inc = ["-I", str(INCLUDE), "-I", str(CSRC)]
@@ -65,8 +85,10 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return str(obj), r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         results = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     log = "\n".join(err for _, err in results)
     (BUILD / "ptxas.log").write_text(log)
     if verbose:
