@@ -369,10 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
         tmem_relinquish();
     }
     grid_dependency_wait();
-    grid_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // A dependent that also wants TMEM may be scheduled from here on: this CTA holds its own.
+    grid_launch_dependents();
     const uint32_t tm = tl->tmem;
 
     const uint64_t total = total_units<kWarpsAll>(p, sh_units, blockIdx.x == 0);
