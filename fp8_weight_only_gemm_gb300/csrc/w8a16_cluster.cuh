@@ -31,10 +31,13 @@ __device__ __forceinline__ void cluster_sync_all() {
     cluster_arrive_release();
     cluster_wait();
 }
-// The FP32 at this CTA's shared address `local`, in the cluster's CTA `rank`.
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t local, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(dsmem_map(local, rank)) : "memory");
+// The 4 FP32 at this CTA's shared address `local`, in the cluster's CTA `rank`.
+__device__ __forceinline__ float4 ld_dsmem_v4f32(uint32_t local, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(dsmem_map(local, rank))
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void st_async_v4f32(uint32_t remote_addr, uint32_t remote_bar, float a,

@@ -112,6 +112,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// The same with the time limit counted from the 64th try: most waits are over by then, and
+// reading the clock takes longer than they do (the 600 to 900 cycles it cost each wait were
+// the longest step of loops whose warps hand tiles to one another).
+__device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag,
+                                              DeviceStatus* st, unsigned int detail) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, st, detail);
+}
+
 // 16-byte asynchronous copy global -> shared through L2 only (the source may have
 // been written by the previous grid), and its group bookkeeping.
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {

@@ -142,7 +142,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
-    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_status, 1);
+    return mbar_wait_for(bar, parity, timeout_ns, abort_flag, &g_kv_attn_status, 1);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {

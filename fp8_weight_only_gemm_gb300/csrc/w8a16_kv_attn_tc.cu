@@ -230,7 +230,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8], fl
 // A wait that gives up `timeout_ns` after it began, and tells the warp as one. (What is
 // rarely run is kept out of line: the loops' code has to stay in the instruction cache.)
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
-    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_kv_attn_tc_status, what);
+    return mbar_wait_for(bar, parity, timeout_ns, abort_flag, &g_kv_attn_tc_status, what);
 }
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag, unsigned what) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             if (elected) {
                 tc_commit(smem_u32(&tl->drain));
                 volatile int never = 0;
-                mbar_wait(smem_u32(&tl->drain), 0, globaltimer_ns() + tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
+                mbar_wait_for(smem_u32(&tl->drain), 0, tmo, &never, &g_kv_attn_tc_status, kWaitDrain);
             }
         } else if (warp == kLookWarp) {
             // ------------------------------------------------- pages and scales

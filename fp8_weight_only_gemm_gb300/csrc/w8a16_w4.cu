@@ -11,11 +11,10 @@
 // contraction's index being free, the activations are paired the same way, and weights never
 // move between lanes.
 //
-// Work. K goes in stages of 256; a CTA takes the rows of a tile and a contiguous range of
-// stages. Codes are copied by TMA, whole boxes, into rings. (Bulk copies of a row a lane are
-// issued lane by lane and cost a warp some 400 instructions a stage.)
-// The sums of a CTA's warps, and those of the CTAs of a cluster that share the rows, are added
-// in a fixed order.
+// Work. A CTA takes the rows of a tile and a contiguous range of K's stages; where tiles alone do
+// not fill the GPU, the CTAs of a cluster share K. Codes are copied by TMA, whole boxes, into rings.
+// (Bulk copies of a row a lane are issued lane by lane and cost a warp some 400 instructions a
+// stage.) The sums of a CTA's warps, and those of a cluster's CTAs, are added in a fixed order.
 //   1 or 2 tokens (w4_stream_kernel). Every warp has a ring and a part of K of its own. The bits of
 //     a nibble, as FP16, are the subnormal number c 2^-24 (or 16 c 2^-24 four bits higher): four
 //     masks and a shift decode a word. The activations become FP16, times a power of two that
@@ -24,10 +23,25 @@
 //     T = sum a, sum (c - z) a = S - z T. Columns that tokens leave unused take other chunks of K
 //     (the operand is zero outside a column's own), so 8 (4) chunks need one set of sums and one
 //     folding.
-//   more (w4_tile_kernel). 128 rows a CTA; its 8 warps share the activations, as they are.
-//     Nibbles are placed under the exponent of 128 (BF16) or 1024 (FP16), and 128 + z (1024 + z)
-//     is subtracted, exactly. From 9 tokens on the pairs are (k, k + 1): two more operations a
-//     word, for none on the activations.
+//   3 to 8 (w4_rows_kernel). The columns are the tokens, so a warp would normalise a chunk of
+//     activations for 32 rows only: they stay as they are and codes become code - z, exactly
+//     (nibbles under the exponent of 128 in BF16, 1024 in FP16; 128 + z, 1024 + z comes off).
+//   more (w4_tc_kernel). m16n8k16 would be issued once for every 8 tokens: tcgen05 instead, 128 rows
+//     of decoded weights in TMEM against 16 or 32 tokens.
+// Where the steps are (us, BF16, 32-bit scales, zero points, groups of 128):
+//                        1024x4096   4096x4096   12288x4096   28672x8192   (N x K)
+//     2 tokens  stream      3.1         5.4         10.4         32.7
+//               rows        3.6         6.5         13.2         37.5
+//     8 tokens  rows        3.8         7.1         13.7         40.5
+//               tc          5.8         8.1         16.3         57.1
+//     16        rows twice  7.6        14.2         27.4         81 (sums of two calls)
+//               tc          6.2         9.1         17.0         58.9
+// Bound by: the stream of bytes at large sizes (28672x8192, one token: 132 MB in 33 us, 4.1 TB/s with groups
+// of 32), the time to the first bytes and the join at small ones. What counts for it is bytes in
+// flight: rings of 192 KB an SM without a barrier between warps stream twice as fast as rings of 96
+// KB behind a CTA's barriers did. With 9 tokens and more, decoding, the products' hand-over and the
+// folding take turns (14336x5120, 32 tokens: 22 us; 17.8 without the decoding, 19.1 without the
+// folding, 10.1 with neither products nor join).
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -78,8 +92,13 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
-    return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, &g_w4_status, 1);
+    return mbar_wait_for(bar, parity, timeout_ns, abort_flag, &g_w4_status, 1);
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
     return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity) || wait_slow(bar, parity, timeout_ns, abort_flag));
@@ -145,18 +164,44 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (w4_tile_kernel) 8 codes -> code - z. zb: (128 + z) twice in BF16, (1024 + z) twice in FP16.
-// NATURAL: pairs (0,1) (2,3) (4,5) (6,7), else (0,4) (1,5) (2,6) (3,7).
-template <bool F16, bool NATURAL>
-__device__ __forceinline__ void decode8(uint32_t q, uint32_t zb, uint32_t (&o)[4]) {
-    const uint32_t odd = q >> 4;   // byte j: code 2 j + 1 low
+// The cluster's (2 or more) CTAs each hold sums [token][ROWS + 4] at `sums`, of TOK tokens at most:
+// adds them in rank order, each CTA a share of the elements, and writes C's rows m0 .. and columns
+// n0 ... All peers are read at once: a load from one takes as long as from eight. C is written after
+// the last arrival, whose release would otherwise wait for the stores.
+template <bool F16, uint32_t ROWS, uint32_t THREADS, uint32_t TOK>
+__device__ __forceinline__ void join_cluster(const W4Args& p, const float* sums, uint32_t rank, uint32_t m0, uint32_t tokens, uint32_t n0) {
+    constexpr uint32_t kIters = ((TOK * (ROWS / 4) + 1) / 2 + THREADS - 1) / THREADS;
+    cluster_sync_all();
+    const uint32_t items = tokens * (ROWS / 4), share = (items + p.split - 1) / p.split, end = min(items, (rank + 1) * share);
+    uint32_t out[kIters][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t y = NATURAL ? prmt(q, odd, i == 0 ? 0x4400u : i == 1 ? 0x5511u : i == 2 ? 0x6622u : 0x7733u) : q >> (4 * i);
-        const uint32_t x = (y & 0x000F000Fu) | (F16 ? 0x64006400u : 0x43004300u);
-        if constexpr (F16) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x), "r"(zb));
-        else asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x), "r"(zb));
+    for (uint32_t it = 0; it < kIters; ++it) {
+        const uint32_t i = rank * share + it * THREADS + threadIdx.x;
+        if (i >= end) continue;
+        const uint32_t at = smem_u32(sums + i / (ROWS / 4) * (ROWS + 4) + i % (ROWS / 4) * 4);
+        float4 v[kMaxSplit];
+#pragma unroll
+        for (uint32_t q = 0; q < kMaxSplit; ++q)
+            if (q < p.split) v[q] = ld_dsmem_v4f32(at, q);
+        float4 x = v[0];
+#pragma unroll
+        for (uint32_t q = 1; q < kMaxSplit; ++q)
+            if (q < p.split) x.x += v[q].x, x.y += v[q].y, x.z += v[q].z, x.w += v[q].w;
+        out[it][0] = pack2<F16>(x.x, x.y), out[it][1] = pack2<F16>(x.z, x.w);
     }
+    __syncwarp();
+    cluster_arrive_release();
+#pragma unroll
+    for (uint32_t it = 0; it < kIters; ++it) {
+        const uint32_t i = rank * share + it * THREADS + threadIdx.x;
+        if (i >= end) continue;
+        const uint32_t r = i % (ROWS / 4) * 4;
+        uint16_t* const c = p.C + static_cast<size_t>(m0 + i / (ROWS / 4)) * p.ldc + n0 + r;
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (n0 + r + e < p.N) c[e] = static_cast<uint16_t>(out[it][e / 2] >> (16 * (e & 1)));
+    }
+    cluster_wait();   // no CTA leaves while another still reads its sums
 }
 
 // ------------------------------------------------------------- 1 or 2 tokens --
@@ -219,7 +264,7 @@ __global__ void __launch_bounds__(kSwThreads, 4) w4_stream_kernel(const W4Args p
         const uint32_t g0 = k_of(i) / G;
 #pragma unroll
         for (uint32_t f = 0; f < kFolds; ++f) {
-            const uint32_t at = min(g0 + (f * kSlots + 2 * c / MP) * 32 / G, groups - kCols);
+            const uint32_t at = min(g0 + (f * kSlots + 2 * c / MP) * 32 / G, groups - kCols);   // (past the end of K sums are 0)
             if (kCols == 1 || pairs) {
 #pragma unroll
                 for (uint32_t r = 0; r < 4; ++r) {
@@ -334,191 +379,481 @@ __global__ void __launch_bounds__(kSwThreads, 4) w4_stream_kernel(const W4Args p
         else if (n0 + r < p.N) p.C[static_cast<size_t>(m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
     }
     if (p.split == 1) return;
-    cluster_sync_all();
-    for (uint32_t i = threadIdx.x + rank * kSwThreads; i < p.M * kSwRows; i += kSwThreads * p.split) {
-        const uint32_t m = i / kSwRows, r = i % kSwRows;
-        float v = 0.f;
-        for (uint32_t q = 0; q < p.split; ++q) v += ld_dsmem_f32(smem_u32(sums + m * kSwRedPitch + r), q);
-        if (n0 + r < p.N) p.C[static_cast<size_t>(m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
+    join_cluster<F16, kSwRows, kSwThreads, MP>(p, sums, rank, 0, p.M, n0);
+}
+
+// ------------------------------------------------------------- 3 to 8 tokens --
+// As the kernel above, a ring of codes and a part of K for every warp; fragments of the
+// activations are loaded from global memory a stage ahead. 32 rows a warp and four stages of 4 KB on
+// 3 CTAs an SM; 64 rows and two stages of 8 KB read the activations half as often and took 0.97 (BF16)
+// and 0.88 (FP16) of the time at 28672x8192 and 8 tokens, but 1.3 at 1024x4096.
+constexpr uint32_t kRwWarps = 4, kRwThreads = 32 * kRwWarps, kRwTiles = 2, kRwRows = 16 * kRwTiles, kRwStages = 4, kRwResident = 3;
+constexpr uint32_t kRwBox = kRwRows * 128, kRwSmem = 1024 + kRwWarps * kRwStages * kRwBox, kRwRedPitch = kRwRows + 4;
+static_assert((kRwWarps + 1) * 8 * kRwRedPitch * 4 <= kRwSmem - 1024, "the sums reuse the rings");
+
+// Scales and zero points of COUNT consecutive groups from `at`; `wide`: they are aligned to be read at once.
+template <bool F16, uint32_t COUNT>
+__device__ __forceinline__ void load_run(const W4Args& p, size_t at, uint32_t valid, bool wide, float (&sc)[COUNT], uint32_t (&zp)[(COUNT + 3) / 4]) {
+    if (wide) {
+        if (p.scale_bytes == 4) {
+            if constexpr (COUNT >= 4) {
+#pragma unroll
+                for (uint32_t i = 0; i < COUNT / 4; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(p.scale + 4 * (at + 4 * i));
+                    sc[4 * i] = v.x, sc[4 * i + 1] = v.y, sc[4 * i + 2] = v.z, sc[4 * i + 3] = v.w;
+                }
+            } else if constexpr (COUNT == 2) {
+                const float2 v = *reinterpret_cast<const float2*>(p.scale + 4 * at);
+                sc[0] = v.x, sc[1] = v.y;
+            } else {
+                sc[0] = *reinterpret_cast<const float*>(p.scale + 4 * at);
+            }
+        } else {
+            if constexpr (COUNT >= 4) {
+#pragma unroll
+                for (uint32_t i = 0; i < COUNT / 4; ++i) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p.scale + 2 * (at + 4 * i));
+                    const float2 a = unpack2<F16>(v.x), b = unpack2<F16>(v.y);
+                    sc[4 * i] = a.x, sc[4 * i + 1] = a.y, sc[4 * i + 2] = b.x, sc[4 * i + 3] = b.y;
+                }
+            } else if constexpr (COUNT == 2) {
+                const float2 v = unpack2<F16>(*reinterpret_cast<const uint32_t*>(p.scale + 2 * at));
+                sc[0] = v.x, sc[1] = v.y;
+            } else {
+                sc[0] = scale_of<F16>(p, at);
+            }
+        }
+        if (p.zeros) {
+            if constexpr (COUNT >= 4) {
+#pragma unroll
+                for (uint32_t i = 0; i < COUNT / 4; ++i) zp[i] = *reinterpret_cast<const uint32_t*>(p.zeros + at + 4 * i);
+            } else if constexpr (COUNT == 2) {
+                zp[0] = *reinterpret_cast<const uint16_t*>(p.zeros + at);
+            } else {
+                zp[0] = p.zeros[at];
+            }
+        }
+        return;
     }
-    cluster_sync_all();   // no CTA leaves while another still reads its sums
+#pragma unroll
+    for (uint32_t i = 0; i < COUNT; ++i) {   // past the end of K sums are 0: the row's last scale does
+        const size_t from = at + min(i, valid - 1);
+        sc[i] = scale_of<F16>(p, from);
+        if (p.zeros) zp[i / 4] = (i % 4 ? zp[i / 4] : 0u) | static_cast<uint32_t>(p.zeros[from]) << (8 * (i % 4));
+    }
+}
+// Whether every run of COUNT groups that starts at a multiple of COUNT is whole and aligned.
+template <uint32_t COUNT>
+__device__ __forceinline__ bool runs_wide(const W4Args& p, uint32_t groups) {
+    return groups % COUNT == 0 && reinterpret_cast<uintptr_t>(p.scale) % (COUNT >= 4 ? 4 * p.scale_bytes : COUNT * p.scale_bytes) == 0;
 }
 
-// --------------------------------------------------------------- more tokens --
-// Warp (wn, wk): rows 32 wn of the tile's 128, half wk (4 chunks) of every stage's K. The rings
-// are the CTA's: a box of codes, and one of 32 values of K of the tokens for each chunk (64-byte
-// rows, with the 64-byte swizzle: no bank is hit twice), filled by a lane of warp 0 when all warps
-// have read a slot.
-constexpr uint32_t kTwThreads = 256, kTwRows = 128, kTwStages = 3, kTwBox = kTwRows * 128, kTwRedPitch = kTwRows + 4;
-constexpr uint32_t tw_stage_bytes(uint32_t tok) { return kTwBox + tok * kStageK * 2; }
-constexpr uint32_t tw_red_bytes(uint32_t tok) { return 2 * tok * kTwRedPitch * 4; }   // halves of K; the first becomes the CTA's sums
-constexpr uint32_t tw_smem_bytes(uint32_t tok) {
-    return 1024 + (kTwStages * tw_stage_bytes(tok) > tw_red_bytes(tok) ? kTwStages * tw_stage_bytes(tok) : tw_red_bytes(tok));
+// 8 codes -> (code - z), pairs (0,4) (1,5) (2,6) (3,7).
+template <bool F16>
+__device__ __forceinline__ void decode_pairs(uint32_t q, uint32_t z, uint32_t (&o)[4]) {
+    if constexpr (F16) {   // 1024 + c, and 1024 + 16 c for what stands four bits higher
+        const uint32_t h = q >> 8, za = (0xE400u + z) * 0x10001u, zb = (0xD400u + 16u * z) * 0x10001u, one = 0x3C003C00u, sixteenth = 0x2C002C00u;
+        const uint32_t x[4] = {(q & 0x000F000Fu) | 0x64006400u, (q & 0x00F000F0u) | 0x64006400u, (h & 0x000F000Fu) | 0x64006400u, (h & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(x[i]), "r"(i & 1 ? sixteenth : one), "r"(i & 1 ? zb : za));
+    } else {
+        const uint32_t zb = (0x4300u + z) * 0x10001u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = (q >> (4 * i) & 0x000F000Fu) | 0x43004300u;
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x), "r"(zb));
+        }
+    }
 }
 
-template <bool F16, uint32_t NT, uint32_t G>
-__global__ void __launch_bounds__(kTwThreads, 2)
-    w4_tile_kernel(const W4Args p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a) {
-    constexpr uint32_t kTok = 8 * NT, kHalfGroups = kStageK / G / 2, kFold = G / 32, kStageBytes = tw_stage_bytes(kTok);
-    constexpr bool kNatural = NT > 1;
+template <bool F16, uint32_t G>
+__global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const W4Args p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap) {
+    constexpr uint32_t kGroups = kStageK / G, kGroupChunks = G / 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t full[kTwStages], empty[kTwStages];
+    __shared__ uint64_t full[kRwWarps][kRwStages];
     __shared__ int abort_flag;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, wn = warp & 3, wk = warp >> 2;
-    const uint32_t rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * kTwRows, m0 = blockIdx.y * kTok;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * kRwRows;
     const uint32_t stages = (p.K + kStageK - 1) / kStageK, groups = p.K / G;
     const uint32_t s_begin = static_cast<uint32_t>(static_cast<uint64_t>(rank) * stages / p.split),
-                   n_stages = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / p.split) - s_begin;
-    const uint32_t tokens = min(kTok, p.M - m0), k_begin = s_begin * kStageK;
-    const size_t row = min(n0 + 32 * wn + lane, p.N - 1);   // whose scales this lane loads
+                   s_end = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / p.split);
+    uint8_t* const boxes = smem + warp * kRwStages * kRwBox;
+    const uint16_t* const a_row = p.A + static_cast<size_t>(min(g, p.M - 1)) * p.lda + 8 * c;
 
-    if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kTwStages; ++i) {
-            mbar_init(smem_u32(&full[i]), 1);
-            mbar_init(smem_u32(&empty[i]), 8);
-        }
-        abort_flag = 0;
+    if (lane == 0) {
+        for (uint32_t i = 0; i < kRwStages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
         fence_barrier_init();
     }
+    if (threadIdx.x == 0) abort_flag = 0;
     if (!p.early) grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
 
-    const auto copy_weights = [&](uint32_t i) {   // (the barrier expects the activations' bytes too)
-        const uint32_t bar = smem_u32(&full[i % kTwStages]);
-        mbar_arrive_expect_tx(bar, kStageBytes);
-        box_load(smem_u32(smem) + i % kTwStages * kStageBytes, &map_w, bar, (k_begin + i * kStageK) / 2, n0);
+    const uint32_t first = s_begin + warp, mine = first < s_end ? (s_end - first + kRwWarps - 1) / kRwWarps : 0;
+    const auto k_of = [&](uint32_t i) { return (first + i * kRwWarps) * kStageK; };
+    const auto copy_weights = [&](uint32_t i) {
+        if (i >= mine || lane != 0) return;
+        const uint32_t at = i % kRwStages, bar = smem_u32(&full[warp][at]);
+        mbar_arrive_expect_tx(bar, kRwBox);
+        box_load(smem_u32(boxes) + at * kRwBox, &map_w, bar, k_of(i) / 2, n0);
     };
-    const auto copy_acts = [&](uint32_t i) {
-        const uint32_t bar = smem_u32(&full[i % kTwStages]), to = smem_u32(smem) + i % kTwStages * kStageBytes + kTwBox;
-#pragma unroll 1
-        for (uint32_t ch = 0; ch < kChunks; ++ch) box_load(to + ch * kTok * 64, &map_a, bar, k_begin + i * kStageK + 32 * ch, m0);
+    uint4 acts[kChunks];
+    const auto load_acts = [&](uint32_t i) {
+        if (i >= mine) return;
+        const uint32_t k0 = k_of(i), chunks = (p.K - k0) / 32;
+#pragma unroll
+        for (uint32_t ch = 0; ch < kChunks; ++ch) acts[ch] = ch < chunks ? *reinterpret_cast<const uint4*>(a_row + k0 + 32 * ch) : make_uint4(0, 0, 0, 0);
     };
-    // scales and zero points of this lane's row, of the groups of the warp's half, a stage ahead
-    float sc[kHalfGroups];
-    uint32_t zp[kHalfGroups];
+    // scales and zero points of the tile's row `lane`, a stage ahead
+    const bool wide = runs_wide<kGroups>(p, groups);
+    float sc[kGroups];
+    uint32_t zp[(kGroups + 3) / 4];
+    const size_t p_row = static_cast<size_t>(min(n0 + lane, p.N - 1)) * groups;
     const auto load_params = [&](uint32_t i) {
-        if (i >= n_stages) return;
-        const uint32_t g0 = (k_begin + i * kStageK) / G + wk * kHalfGroups;
-#pragma unroll
-        for (uint32_t q = 0; q < kHalfGroups; ++q) {   // past the end of K activations are 0
-            const size_t at = row * groups + min(g0 + q, groups - 1);
-            sc[q] = scale_of<F16>(p, at);
-            if (p.zeros) zp[q] = p.zeros[at];
-        }
+        if (i >= mine) return;
+        const uint32_t g0 = k_of(i) / G;
+        load_run<F16, kGroups>(p, p_row + g0, min(kGroups, groups - g0), wide, sc, zp);
     };
 #pragma unroll
-    for (uint32_t q = 0; q < kHalfGroups; ++q) zp[q] = 8u;
-    const uint32_t ahead = min(n_stages, kTwStages);
-    if (threadIdx.x == 0)
-        for (uint32_t i = 0; i < ahead; ++i) copy_weights(i);
+    for (uint32_t q = 0; q < (kGroups + 3) / 4; ++q) zp[q] = 0x08080808u;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kRwStages; ++i) copy_weights(i);
     load_params(0);
     if (p.early) grid_dependency_wait();
-    if (threadIdx.x == 0)
-        for (uint32_t i = 0; i < ahead; ++i) copy_acts(i);
+    load_acts(0);
 
-    float acc[2][NT][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (uint32_t n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
+    float acc[kRwTiles][4] = {};
 #pragma unroll 1
-    for (uint32_t i = 0; i < n_stages; ++i) {
-        const uint32_t at = i % kTwStages, parity = (i / kTwStages) & 1;
-        float cs[kHalfGroups];
-        uint32_t cz[kHalfGroups];
+    for (uint32_t i = 0; i < mine; ++i) {
+        const uint32_t at = i % kRwStages;
+        uint4 b[kChunks];
+        float cs[kGroups];
+        uint32_t cz[(kGroups + 3) / 4];
 #pragma unroll
-        for (uint32_t q = 0; q < kHalfGroups; ++q) {
-            cs[q] = sc[q];
-            // 128 + z in BF16 (0x4300 + z), 1024 + z in FP16 (0x6400 + z), twice
-            cz[q] = ((F16 ? 0x6400u : 0x4300u) + zp[q]) * 0x10001u;
-        }
+        for (uint32_t ch = 0; ch < kChunks; ++ch) b[ch] = acts[ch];
+#pragma unroll
+        for (uint32_t q = 0; q < kGroups; ++q) cs[q] = sc[q];
+#pragma unroll
+        for (uint32_t q = 0; q < (kGroups + 3) / 4; ++q) cz[q] = zp[q];
         load_params(i + 1);
-        if (!wait_warp(smem_u32(&full[at]), parity, p.timeout_ns, &abort_flag)) break;
-        const uint8_t* const w = smem + at * kStageBytes + (32 * wn + g) * 128 + 4 * c;
-        const uint8_t* const a = smem + at * kStageBytes + kTwBox + 4 * wk * kTok * 64 + g * 64 + ((c ^ (g >> 1 & 3)) << 4);
+        load_acts(i + 1);
+        if (!wait_warp(smem_u32(&full[warp][at]), (i / kRwStages) & 1, p.timeout_ns, &abort_flag)) break;
+        const uint8_t* const w = boxes + at * kRwBox + g * 128 + 4 * c;
 #pragma unroll
-        for (uint32_t q = 0; q < kHalfGroups; ++q) {
-            uint32_t z[4];
-            float f[4];
+        for (uint32_t q = 0; q < kGroups; ++q) {
+            float part[kRwTiles][4] = {};
+            uint32_t z[kRwTiles][2];
 #pragma unroll
-            for (uint32_t r = 0; r < 4; ++r) z[r] = __shfl_sync(0xFFFFFFFFu, cz[q], 8 * r + g), f[r] = __shfl_sync(0xFFFFFFFFu, cs[q], 8 * r + g);
-            float part[2][NT][4];
+            for (uint32_t t = 0; t < kRwTiles; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (uint32_t r = 0; r < 2; ++r)
+                    z[t][r] = __shfl_sync(0xFFFFFFFFu, cz[q / 4] >> (8 * (q % 4)), 16 * t + 8 * r + g) & 0xFFu;
 #pragma unroll
-                for (uint32_t n = 0; n < NT; ++n) part[t][n][0] = part[t][n][1] = part[t][n][2] = part[t][n][3] = 0.f;
+            for (uint32_t ch = q * kGroupChunks; ch < (q + 1) * kGroupChunks; ++ch) {
+                const uint32_t b0 = prmt(b[ch].x, b[ch].z, 0x5410), b1 = prmt(b[ch].x, b[ch].z, 0x7632), b2 = prmt(b[ch].y, b[ch].w, 0x5410),
+                               b3 = prmt(b[ch].y, b[ch].w, 0x7632);
 #pragma unroll
-            for (uint32_t ch = q * kFold; ch < (q + 1) * kFold; ++ch) {
-                uint32_t x[4][4];
+                for (uint32_t t = 0; t < kRwTiles; ++t) {
+                    uint32_t x[2][4];
 #pragma unroll
-                for (uint32_t r = 0; r < 4; ++r) decode8<F16, kNatural>(*reinterpret_cast<const uint32_t*>(w + 1024 * r + (((4 * wk + ch) ^ g) << 4)), z[r], x[r]);
-                uint32_t f0[2][4], f1[2][4];
-#pragma unroll
-                for (uint32_t t = 0; t < 2; ++t)
-#pragma unroll
-                    for (uint32_t r = 0; r < 2; ++r) f0[t][r] = x[2 * t + r][0], f0[t][2 + r] = x[2 * t + r][1], f1[t][r] = x[2 * t + r][2], f1[t][2 + r] = x[2 * t + r][3];
-#pragma unroll
-                for (uint32_t n = 0; n < NT; ++n) {
-                    uint4 b = *reinterpret_cast<const uint4*>(a + (ch * kTok + 8 * n) * 64);
-                    if constexpr (!kNatural) b = make_uint4(prmt(b.x, b.z, 0x5410), prmt(b.x, b.z, 0x7632), prmt(b.y, b.w, 0x5410), prmt(b.y, b.w, 0x7632));
-#pragma unroll
-                    for (uint32_t t = 0; t < 2; ++t) {
-                        mma_16816<F16>(part[t][n], f0[t], b.x, b.y);
-                        mma_16816<F16>(part[t][n], f1[t], b.z, b.w);
-                    }
+                    for (uint32_t r = 0; r < 2; ++r) decode_pairs<F16>(*reinterpret_cast<const uint32_t*>(w + 2048 * t + 1024 * r + ((ch ^ g) << 4)), z[t][r], x[r]);
+                    const uint32_t f0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]}, f1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
+                    mma_16816<F16>(part[t], f0, b0, b1);
+                    mma_16816<F16>(part[t], f1, b2, b3);
                 }
             }
 #pragma unroll
-            for (uint32_t n = 0; n < NT; ++n)
+            for (uint32_t t = 0; t < kRwTiles; ++t)
 #pragma unroll
-                for (uint32_t r = 0; r < 4; ++r) {
-                    acc[r / 2][n][2 * (r % 2)] = fmaf(f[r], part[r / 2][n][2 * (r % 2)], acc[r / 2][n][2 * (r % 2)]);
-                    acc[r / 2][n][2 * (r % 2) + 1] = fmaf(f[r], part[r / 2][n][2 * (r % 2) + 1], acc[r / 2][n][2 * (r % 2) + 1]);
+                for (uint32_t r = 0; r < 2; ++r) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, cs[q], 16 * t + 8 * r + g);
+                    acc[t][2 * r] = fmaf(f, part[t][2 * r], acc[t][2 * r]), acc[t][2 * r + 1] = fmaf(f, part[t][2 * r + 1], acc[t][2 * r + 1]);
                 }
         }
-        // this slot has been read by all lanes of the warp; the one before it is refilled once all warps
-        // are past it (by then most are, and warp 0 has a stage of its own left)
+        // all lanes have read the slot: it may be overwritten
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[at]));
-        if (warp == 0 && i > 0 && i - 1 + kTwStages < n_stages) {
-            if (!wait_warp(smem_u32(&empty[(i - 1) % kTwStages]), ((i - 1) / kTwStages) & 1, p.timeout_ns, &abort_flag)) break;
-            if (lane == 0) {
-                copy_weights(i - 1 + kTwStages);
-                copy_acts(i - 1 + kTwStages);
+        copy_weights(i + kRwStages);
+    }
+
+    // ---- sums of the warps, then of the cluster's CTAs, in order
+    __syncthreads();   // every warp is done with its ring, which the sums reuse
+    float* const red = reinterpret_cast<float*>(smem);                       // [warp][8 columns][kRedPitch]
+    float* const sums = red + kRwWarps * 8 * kRwRedPitch;                // [token][kRedPitch]
+#pragma unroll
+    for (uint32_t t = 0; t < kRwTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[(warp * 8 + 2 * c + (e & 1)) * kRwRedPitch + 16 * t + 8 * (e >> 1) + g] = acc[t][e];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < p.M * kRwRows; i += kRwThreads) {
+        const uint32_t m = i / kRwRows, r = i % kRwRows;
+        float v = 0.f;
+#pragma unroll
+        for (uint32_t w = 0; w < kRwWarps; ++w) v += red[(w * 8 + m) * kRwRedPitch + r];
+        if (p.split > 1) sums[m * kRwRedPitch + r] = v;
+        else if (n0 + r < p.N) p.C[static_cast<size_t>(m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
+    }
+    if (p.split > 1) join_cluster<F16, kRwRows, kRwThreads, 8>(p, sums, rank, 0, p.M, n0);
+}
+
+// --------------------------------------------------------------- more tokens --
+// D[row][token] of a chunk of kCk values of K (no more than a group) is one run of tcgen05.mma
+// with the decoded weights in TMEM as A (lane = weight row, column j = values 2 j and 2 j + 1)
+// and the activations, as TMA wrote them, as B. Warps 0-3 decode, a thread a row, and add
+// scale * D to the row's sums; warp 4 copies and issues. Two slots of TMEM: while a chunk's
+// product runs the next one is decoded, and a slot is free again once its sums have been read.
+constexpr uint32_t kTcThreads4 = 160, kTcRows4 = 128, kTcStageK = 128, kTcWBytes = kTcRows4 * kTcStageK / 2, kTcResident = 4;
+constexpr uint32_t kTcTmemCols = 128, kTcRedPitch = kTcRows4 + 4;
+template <uint32_t NT, uint32_t G>
+struct TcCfg {
+    static constexpr uint32_t kTok = NT;                                  // the product's columns
+    static constexpr uint32_t kCk = G < 64 ? G : 64, kPerStage = kTcStageK / kCk, kACols = kCk / 2;
+    static constexpr uint32_t kStageGroups = kTcStageK / G;
+    static constexpr uint32_t kSlotCols = kACols + kTok;
+    static constexpr uint32_t kActBytes = kTok * 128;                       // 64 values of K
+    static constexpr uint32_t kStageBytes = kTcWBytes + 2 * kActBytes;
+    static constexpr uint32_t kStages = NT > 16 ? 3 : 4;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes;
+    static_assert(2 * kSlotCols <= kTcTmemCols && kPerStage % 2 == 0, "slots");
+    static_assert(kTok * kTcRedPitch * 4 <= kStages * kStageBytes, "the sums reuse the ring");
+    static_assert(kTcResident * (kSmem + 2048) <= 228 * 1024, "CTAs of an SM");
+};
+
+// 8 codes of a row -> (code - z), pairs (0,1) (2,3) (4,5) (6,7). The bits of a nibble go under the
+// exponent of 128 (BF16) or, the even one of a pair, 1024 and the odd one, times 16, 1024 (FP16: no
+// shift); what comes off is exact in both.
+template <bool F16>
+__device__ __forceinline__ uint32_t zero_operand(uint32_t z) {
+    return F16 ? (0xE400u + z) | (0xD400u + 16u * z) << 16    // -(1024 + z), -(64 + z)
+               : (0x4300u + z) * 0x10001u;                    // 128 + z
+}
+template <bool F16>
+__device__ __forceinline__ void decode_row8(uint32_t q, uint32_t zb, uint32_t* o) {
+    const uint32_t odd = F16 ? 0x64646464u : q >> 4;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        if constexpr (F16) {
+            const uint32_t x = prmt(q, odd, 0x4040u + 0x0101u * i) & 0x64F0640Fu;
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(x), "r"(0x2C003C00u), "r"(zb));   // (1/16, 1)
+        } else {
+            const uint32_t x = (prmt(q, odd, 0x4400u + 0x1111u * i) & 0x000F000Fu) | 0x43004300u;
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x), "r"(zb));
+        }
+    }
+}
+
+template <bool F16, uint32_t NT, uint32_t G>
+__global__ void __launch_bounds__(kTcThreads4, kTcResident)
+    w4_tc_kernel(const W4Args p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a) {
+    using C = TcCfg<NT, G>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ uint64_t full[C::kStages], a_full[2], d_full[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 4) {   // first of all: the SM starts no other CTA until the permit is back (0.5 us a CTA)
+        tmem_alloc(smem_u32(&tmem_slot), kTcTmemCols);
+        tmem_relinquish();
+    } else if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_a);
+        for (uint32_t i = 0; i < C::kStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&a_full[i]), 4);
+            mbar_init(smem_u32(&d_full[i]), 1);
+        }
+        mbar_init(smem_u32(&drain), 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    const uint32_t rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * kTcRows4, m0 = blockIdx.y * C::kTok;
+    const uint32_t stages = (p.K + kTcStageK - 1) / kTcStageK, groups = p.K / G;
+    const uint32_t s_begin = static_cast<uint32_t>(static_cast<uint64_t>(rank) * stages / p.split),
+                   n_stages = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / p.split) - s_begin;
+    const uint32_t tokens = min(C::kTok, p.M - m0), k_begin = s_begin * kTcStageK;
+
+    if (!p.early) grid_dependency_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // A dependent that also wants TMEM may be scheduled from here on: this CTA holds its own.
+    grid_launch_dependents();
+    const uint32_t tm = tmem_slot;
+    uint64_t acc[C::kTok / 2] = {};   // FP32 pairs
+
+    if (warp == 4) {
+        // The whole warp goes through the loop, on broadcast addresses, and one elected lane issues: so
+        // descriptors are formed in uniform registers (a lane of its own took 430 cycles for 4 products).
+        const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0), tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
+        const uint64_t desc = smem_desc_kmajor_sw128(base + kTcWBytes);
+        const bool elected = elect_one();
+        const auto copy_weights = [&](uint32_t s) {   // (the barrier expects the activations' bytes too)
+            const uint32_t bar = smem_u32(&full[s % C::kStages]);
+            mbar_arrive_expect_tx(bar, C::kStageBytes);
+            box_load(base + s % C::kStages * C::kStageBytes, &map_w, bar, (k_begin + s * kTcStageK) / 2, n0);
+        };
+        const auto copy_acts = [&](uint32_t s) {
+            const uint32_t bar = smem_u32(&full[s % C::kStages]), to = base + s % C::kStages * C::kStageBytes + kTcWBytes;
+            box_load(to, &map_a, bar, k_begin + s * kTcStageK, m0);
+            box_load(to + C::kActBytes, &map_a, bar, k_begin + s * kTcStageK + 64, m0);
+        };
+        const uint32_t ahead = min(n_stages, C::kStages);
+        if (elected)
+            for (uint32_t s = 0; s < ahead; ++s) copy_weights(s);
+        if (p.early) grid_dependency_wait();
+        if (elected)
+            for (uint32_t s = 0; s < ahead; ++s) copy_acts(s);
+        __syncwarp();
+        constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTok) & ~(F16 ? (1u << 7 | 1u << 10) : 0u);
+        uint32_t issued = ahead;   // stages
+        bool ok = true;
+        uint32_t s = 0;
+#pragma unroll 1
+        for (; ok && s < n_stages; ++s) {
+            const uint32_t at = s % C::kStages;
+#pragma unroll
+            for (uint32_t j = 0; j < C::kPerStage; ++j) {
+                const uint32_t i = s * C::kPerStage + j, slot = j & 1;
+                ok = ok && wait_warp(smem_u32(&a_full[slot]), (i >> 1) & 1, p.timeout_ns, &abort_flag);
+                if (j == 0) ok = ok && wait_warp(smem_u32(&full[at]), (s / C::kStages) & 1, p.timeout_ns, &abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t k = j * C::kCk;
+                const uint64_t b = desc + at * (C::kStageBytes >> 4) + ((k / 64 * C::kActBytes + k % 64 * 2) >> 4);
+                const uint32_t tA = tmu + slot * C::kSlotCols, tD = tA + C::kACols;
+                if (elected) {
+#pragma unroll
+                    for (uint32_t e = 0; e < C::kCk / 16; ++e) tc_mma_a_tmem(tD, tA + 8 * e, b + 2 * e, kIdesc, e ? 1u : 0u);
+                    tc_commit(smem_u32(&d_full[slot]));
+                }
+                __syncwarp();
+                // The stage before this one has been decoded; once its last product is done it is refilled.
+                if (j == 0 && s > 0 && issued < n_stages) {
+                    ok = wait_warp(smem_u32(&d_full[1]), ((i - 1) >> 1) & 1, p.timeout_ns, &abort_flag);
+                    if (!ok) break;
+                    if (elected) {
+                        copy_weights(issued);
+                        copy_acts(issued);
+                    }
+                    ++issued;
+                    __syncwarp();
+                }
             }
-            __syncwarp();
+        }
+        // Nothing of this CTA's is in flight when it leaves: products, and (after a wait that gave up) copies.
+        if (elected) {
+            tc_commit(smem_u32(&drain));
+            mbar_wait_for(smem_u32(&drain), 0, p.timeout_ns, &abort_flag, &g_w4_status, 2);
+            if (!ok) {
+                int none = 0;   // not the raised flag: these waits have their own limit
+                for (uint32_t q = s > 0 ? s - 1 : 0; q < issued; ++q)
+                    mbar_wait_for(smem_u32(&full[q % C::kStages]), (q / C::kStages) & 1, p.timeout_ns, &none, &g_w4_status, 3);
+            }
+        }
+        __syncwarp();
+    } else {
+        const uint32_t row = threadIdx.x, lanes = (warp * 32) << 16;
+        const size_t p_row = static_cast<size_t>(min(n0 + row, p.N - 1)) * groups;
+        const bool wide = runs_wide<C::kStageGroups>(p, groups);
+        float sc[C::kStageGroups];
+        uint32_t zp = 0x08080808u;
+        const auto load_params = [&](uint32_t s) {   // a stage ahead
+            if (s >= n_stages) return;
+            const uint32_t g0 = (k_begin + s * kTcStageK) / G;
+            uint32_t z[1] = {zp};
+            load_run<F16, C::kStageGroups>(p, p_row + g0, min(C::kStageGroups, groups - g0), wide, sc, z);
+            zp = z[0];
+        };
+        load_params(0);
+        float f[2] = {};   // scales of the slots' chunks
+        const auto done = [&](uint32_t i, uint32_t slot) {   // the product of chunk i, in this slot
+            const bool ok = wait_warp(smem_u32(&d_full[slot]), (i >> 1) & 1, p.timeout_ns, &abort_flag);
+            tc_fence_after();
+            return ok;
+        };
+        const auto fold = [&](uint32_t slot) {   // sums += scale * D
+            const uint64_t ff = pack_f32x2(f[slot], f[slot]);
+#pragma unroll
+            for (uint32_t t = 0; t < C::kTok; t += 16) {
+                float d[2][8];
+                const uint32_t tD = tm + slot * C::kSlotCols + C::kACols + lanes + t;
+                tmem_ld_32x32b_x8(tD, d[0]);
+                tmem_ld_32x32b_x8(tD + 8, d[1]);
+                tc_wait_ld();
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    acc[t / 2 + e] = fma_f32x2(ff, pack_f32x2(d[e / 4][e % 4 * 2], d[e / 4][e % 4 * 2 + 1]), acc[t / 2 + e]);
+            }
+        };
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t s = 0; ok && s < n_stages; ++s) {
+            const uint32_t at = s % C::kStages;
+            float cs[C::kStageGroups];
+            uint32_t cz[C::kStageGroups];
+#pragma unroll
+            for (uint32_t q = 0; q < C::kStageGroups; ++q) cs[q] = sc[q], cz[q] = zero_operand<F16>(zp >> (8 * q) & 0xFFu);
+            load_params(s + 1);
+            ok = wait_warp(smem_u32(&full[at]), (s / C::kStages) & 1, p.timeout_ns, &abort_flag);
+            const uint8_t* const w = smem + at * C::kStageBytes + row * 64;
+#pragma unroll
+            for (uint32_t j = 0; j < C::kPerStage; ++j) {
+                const uint32_t i = s * C::kPerStage + j, slot = j & 1, q = j * C::kCk / G;
+                uint4 v = *reinterpret_cast<const uint4*>(w + (((j * C::kCk / 32) ^ (row >> 1 & 3)) << 4));
+                if (i >= 2) ok = ok && done(i - 2, slot);
+                if (!ok) break;
+                if (i >= 2) fold(slot);
+                const uint32_t tA = tm + slot * C::kSlotCols + lanes;
+#pragma unroll
+                for (uint32_t h = 0; h < C::kCk / 32; ++h) {
+                    if (h > 0) v = *reinterpret_cast<const uint4*>(w + (((j * C::kCk / 32 + h) ^ (row >> 1 & 3)) << 4));
+                    uint32_t o[16];
+                    decode_row8<F16>(v.x, cz[q], o);
+                    decode_row8<F16>(v.y, cz[q], o + 4);
+                    decode_row8<F16>(v.z, cz[q], o + 8);
+                    decode_row8<F16>(v.w, cz[q], o + 12);
+                    tmem_st_32x32b_x16(tA + 16 * h, o);
+                }
+                f[slot] = cs[q];
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&a_full[slot]));
+            }
+        }
+        if (n_stages > 0) {   // the last two chunks
+            const uint32_t n = n_stages * C::kPerStage;
+            ok = ok && done(n - 2, 0);
+            if (ok) fold(0);
+            ok = ok && done(n - 1, 1);
+            if (ok) fold(1);
         }
     }
 
-    // ---- sums of the halves, then of the cluster's CTAs, in order
-    __syncthreads();   // every warp is done with the rings, which the sums reuse
-    float* const red = reinterpret_cast<float*>(smem);   // [half][token][kTwRedPitch]
+    // ---- the rows' sums, then those of the cluster's CTAs, in order
+    tc_fence_before();
+    __syncthreads();   // products and copies are done: the sums reuse the ring, and TMEM goes back before any wait for a peer
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tm, kTcTmemCols);
+    float* const red = reinterpret_cast<float*>(smem);   // [token][kTcRedPitch]
+    if (warp < 4) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                red[(wk * kTok + 8 * n + 2 * c + (e & 1)) * kTwRedPitch + 32 * wn + 16 * t + 8 * (e >> 1) + g] = acc[t][n][e];
+        for (uint32_t t = 0; t < C::kTok; t += 2) {
+            const float2 x = unpack_f32x2(acc[t / 2]);
+            red[t * kTcRedPitch + threadIdx.x] = x.x, red[(t + 1) * kTcRedPitch + threadIdx.x] = x.y;
+        }
+    }
+    if (p.split > 1) {
+        join_cluster<F16, kTcRows4, kTcThreads4, C::kTok>(p, red, rank, m0, tokens, n0);
+        return;
+    }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < tokens * kTwRows; i += kTwThreads) {
-        const uint32_t m = i / kTwRows, r = i % kTwRows;
-        const float v = red[m * kTwRedPitch + r] + red[(kTok + m) * kTwRedPitch + r];
-        if (p.split > 1) red[m * kTwRedPitch + r] = v;   // this thread's own element
-        else if (n0 + r < p.N) p.C[static_cast<size_t>(m0 + m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
+    for (uint32_t i = threadIdx.x; i < tokens * kTcRows4; i += kTcThreads4) {
+        const uint32_t m = i / kTcRows4, r = i % kTcRows4;
+        if (n0 + r < p.N) p.C[static_cast<size_t>(m0 + m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(red[m * kTcRedPitch + r], 0.f));
     }
-    if (p.split == 1) return;
-    cluster_sync_all();
-    for (uint32_t i = threadIdx.x + rank * kTwThreads; i < tokens * kTwRows; i += kTwThreads * p.split) {
-        const uint32_t m = i / kTwRows, r = i % kTwRows;
-        float v = 0.f;
-        for (uint32_t q = 0; q < p.split; ++q) v += ld_dsmem_f32(smem_u32(red + m * kTwRedPitch + r), q);
-        if (n0 + r < p.N) p.C[static_cast<size_t>(m0 + m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
-    }
-    cluster_sync_all();   // no CTA leaves while another still reads its sums
 }
 
 // Launches `kernel` on clusters of a.split CTAs along x, as a programmatic dependent.
@@ -540,7 +875,7 @@ cudaError_t launch_clusters(void (*kernel)(const W4Args, const CUtensorMap, cons
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = a.split > 1 ? 2 : 1;   // (a cluster of one CTA starts 11 ns after another: 600 CTAs in 0.7 us, 0.1 without)
     return cudaLaunchKernelEx(&cfg, kernel, a, map_w, map_a);
 }
 
@@ -554,10 +889,10 @@ uint32_t choose_split(uint64_t tiles, uint64_t slots, uint32_t stages, uint32_t 
 // The descriptors of a launch; false with a message.
 struct Maps {
     CUtensorMap w, a;
-    bool make(const W4Args& p, uint32_t rows, uint32_t tokens, std::string* err) {
+    bool make(const W4Args& p, uint32_t rows, uint32_t bytes, uint32_t tokens, uint32_t ks, std::string* err) {
         std::memset(&a, 0, sizeof a);
-        return tensor_map_2d(p.W, p.N, p.K / 2, p.K / 2, 1, rows, 128, &w, err) &&
-               (tokens == 0 || tensor_map_2d(p.A, p.M, p.K, 2ull * p.lda, 2, tokens, 32, &a, err));
+        return tensor_map_2d(p.W, p.N, p.K / 2, p.K / 2, 1, rows, bytes, &w, err) &&
+               (tokens == 0 || tensor_map_2d(p.A, p.M, p.K, 2ull * p.lda, 2, tokens, ks, &a, err));
     }
 };
 
@@ -568,24 +903,33 @@ cudaError_t launch_stream(W4Args a, int sms, cudaStream_t s, std::string* err) {
     // a stage a warp at least
     a.split = choose_split(tiles, static_cast<uint64_t>(sms) * resident, (a.K + kStageK - 1) / kStageK, kSwWarps);
     Maps m;
-    if (!m.make(a, kSwRows, 0, err)) return cudaErrorInvalidValue;
+    if (!m.make(a, kSwRows, 128, 0, 0, err)) return cudaErrorInvalidValue;
     return launch_clusters(w4_stream_kernel<F16, MP, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kSwThreads, smem, s);
 }
-template <bool F16, uint32_t NT, uint32_t G>
-cudaError_t launch_tile(W4Args a, int sms, cudaStream_t s, std::string* err) {
-    const uint32_t tiles = (a.N + kTwRows - 1) / kTwRows, tok_tiles = (a.M + 8 * NT - 1) / (8 * NT);
-    a.split = choose_split(static_cast<uint64_t>(tiles) * tok_tiles, 2ull * sms, (a.K + kStageK - 1) / kStageK, 2);
+template <bool F16, uint32_t G>
+cudaError_t launch_rows(W4Args a, int sms, cudaStream_t s, std::string* err) {
+    const uint32_t tiles = (a.N + kRwRows - 1) / kRwRows;
+    a.split = choose_split(tiles, static_cast<uint64_t>(sms) * kRwResident, (a.K + kStageK - 1) / kStageK, kRwWarps);
     Maps m;
-    if (!m.make(a, kTwRows, 8 * NT, err)) return cudaErrorInvalidValue;
-    return launch_clusters(w4_tile_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kTwThreads, tw_smem_bytes(8 * NT), s);
+    if (!m.make(a, kRwRows, 128, 0, 0, err)) return cudaErrorInvalidValue;
+    return launch_clusters(w4_rows_kernel<F16, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kRwThreads, kRwSmem, s);
+}
+template <bool F16, uint32_t NT, uint32_t G>
+cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
+    using C = TcCfg<NT, G>;
+    const uint32_t tiles = (a.N + kTcRows4 - 1) / kTcRows4, tok_tiles = (a.M + NT - 1) / NT;
+    a.split = choose_split(static_cast<uint64_t>(tiles) * tok_tiles, static_cast<uint64_t>(kTcResident) * sms, (a.K + kTcStageK - 1) / kTcStageK, 2);
+    Maps m;
+    if (!m.make(a, kTcRows4, kTcStageK / 2, C::kTok, 64, err)) return cudaErrorInvalidValue;
+    return launch_clusters(w4_tc_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kTcThreads4, C::kSmem, s);
 }
 template <bool F16, uint32_t G>
 cudaError_t launch_tokens(const W4Args& a, int sms, cudaStream_t s, std::string* err) {
     return a.M == 1    ? launch_stream<F16, 1, G>(a, sms, s, err)
            : a.M == 2  ? launch_stream<F16, 2, G>(a, sms, s, err)
-           : a.M <= 8  ? launch_tile<F16, 1, G>(a, sms, s, err)
-           : a.M <= 16 ? launch_tile<F16, 2, G>(a, sms, s, err)
-                       : launch_tile<F16, 4, G>(a, sms, s, err);
+           : a.M <= 8  ? launch_rows<F16, G>(a, sms, s, err)
+           : a.M <= 16 ? launch_tc<F16, 16, G>(a, sms, s, err)
+                       : launch_tc<F16, 32, G>(a, sms, s, err);
 }
 template <bool F16>
 cudaError_t launch_group(const W4Args& a, uint32_t group, int sms, cudaStream_t s, std::string* err) {

@@ -139,3 +139,15 @@ def test_refusals(w8):
         w8.gemm_w4(A, W, scale, flags=64)
     with pytest.raises(w8.W8A16Error):
         w8.gemm_w4(torch.empty(2, 260, dtype=torch.bfloat16, device="cuda")[:, 4:], W, scale)   # alignment
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 2, 5, 20])
+def test_nonfinite_scales_stay_in_their_column(w8, M, group):
+    K = 9 * group   # the last stage of K is not full
+    A, W, scale, z = make(M, 40, K, group, "bf16", True, True, seed=M)
+    scale[7, -1] = float("inf")
+    scale[30, 2] = float("nan")
+    got = w8.gemm_w4(A.cuda(), W.cuda(), scale.cuda(), zeros=z.cuda()).double().cpu().numpy()
+    assert not np.isfinite(got[:, [7, 30]]).any()
+    assert np.isfinite(np.delete(got, [7, 30], 1)).all()
