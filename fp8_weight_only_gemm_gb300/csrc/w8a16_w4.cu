@@ -23,9 +23,10 @@
 //     T = sum a, sum (c - z) a = S - z T. Columns that tokens leave unused take other chunks of K
 //     (the operand is zero outside a column's own), so 8 (4) chunks need one set of sums and one
 //     folding.
-//   3 to 8 (w4_rows_kernel). The columns are the tokens, so a warp would normalise a chunk of
-//     activations for 32 rows only: they stay as they are and codes become code - z, exactly
-//     (nibbles under the exponent of 128 in BF16, 1024 in FP16; 128 + z, 1024 + z comes off).
+//   3 to 8, and up to 16 of a small product (w4_rows_kernel). The columns are the tokens, so a warp
+//     would normalise a chunk of activations for 32 rows only: they stay as they are and codes
+//     become code - z, exactly (nibbles under the exponent of 128 in BF16, 1024 in FP16; 128 + z,
+//     1024 + z comes off).
 //   more (w4_tc_kernel). m16n8k16 would be issued once for every 8 tokens: tcgen05 instead, 128 rows
 //     of decoded weights in TMEM against 16 or 32 tokens.
 // Where the steps are (us, BF16, 32-bit scales, zero points, groups of 128):
@@ -34,8 +35,9 @@
 //               rows        3.6         6.5         13.2         37.5
 //     8 tokens  rows        3.8         7.1         13.7         40.5
 //               tc          5.8         8.1         16.3         57.1
-//     16        rows twice  7.6        14.2         27.4         81 (sums of two calls)
-//               tc          6.2         9.1         17.0         58.9
+//     16        rows        4.4         7.6         18.9         59.0
+//               tc          6.3         9.1         17.0         58.7
+// (12288 rows are 1.3 rounds of tiles there.)
 // Bound by: the stream of bytes at large sizes (28672x8192, one token: 132 MB in 33 us, 4.1 TB/s with groups
 // of 32), the time to the first bytes and the join at small ones. What counts for it is bytes in
 // flight: rings of 192 KB an SM without a barrier between warps stream twice as fast as rings of 96
@@ -382,14 +384,18 @@ __global__ void __launch_bounds__(kSwThreads, 4) w4_stream_kernel(const W4Args p
     join_cluster<F16, kSwRows, kSwThreads, MP>(p, sums, rank, 0, p.M, n0);
 }
 
-// ------------------------------------------------------------- 3 to 8 tokens --
+// ------------------------------------------------------------ 3 to 16 tokens --
 // As the kernel above, a ring of codes and a part of K for every warp; fragments of the
 // activations are loaded from global memory a stage ahead. 32 rows a warp and four stages of 4 KB on
 // 3 CTAs an SM; 64 rows and two stages of 8 KB read the activations half as often and took 0.97 (BF16)
 // and 0.88 (FP16) of the time at 28672x8192 and 8 tokens, but 1.3 at 1024x4096.
-constexpr uint32_t kRwWarps = 4, kRwThreads = 32 * kRwWarps, kRwTiles = 2, kRwRows = 16 * kRwTiles, kRwStages = 4, kRwResident = 3;
-constexpr uint32_t kRwBox = kRwRows * 128, kRwSmem = 1024 + kRwWarps * kRwStages * kRwBox, kRwRedPitch = kRwRows + 4;
-static_assert((kRwWarps + 1) * 8 * kRwRedPitch * 4 <= kRwSmem - 1024, "the sums reuse the rings");
+constexpr uint32_t kRwWarps = 4, kRwThreads = 32 * kRwWarps, kRwTiles = 2, kRwRows = 16 * kRwTiles;
+constexpr uint32_t kRwBox = kRwRows * 128, kRwRedPitch = kRwRows + 4;
+template <uint32_t NT>
+struct RwCfg {
+    static constexpr uint32_t kTok = 8 * NT, kStages = NT == 1 ? 4 : 6, kResident = NT == 1 ? 3 : 2, kSmem = 1024 + kRwWarps * kStages * kRwBox;
+    static_assert((kRwWarps + 1) * kTok * kRwRedPitch * 4 <= kSmem - 1024, "the sums reuse the rings");
+};
 
 // Scales and zero points of COUNT consecutive groups from `at`; `wide`: they are aligned to be read at once.
 template <bool F16, uint32_t COUNT>
@@ -466,9 +472,9 @@ __device__ __forceinline__ void decode_pairs(uint32_t q, uint32_t z, uint32_t (&
     }
 }
 
-template <bool F16, uint32_t G>
-__global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const W4Args p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap) {
-    constexpr uint32_t kGroups = kStageK / G, kGroupChunks = G / 32;
+template <bool F16, uint32_t NT, uint32_t G>
+__global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kernel(const W4Args p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap) {
+    constexpr uint32_t kGroups = kStageK / G, kGroupChunks = G / 32, kRwStages = RwCfg<NT>::kStages, kTok = RwCfg<NT>::kTok;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t full[kRwWarps][kRwStages];
@@ -479,7 +485,9 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
     const uint32_t s_begin = static_cast<uint32_t>(static_cast<uint64_t>(rank) * stages / p.split),
                    s_end = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / p.split);
     uint8_t* const boxes = smem + warp * kRwStages * kRwBox;
-    const uint16_t* const a_row = p.A + static_cast<size_t>(min(g, p.M - 1)) * p.lda + 8 * c;
+    const uint16_t* a_row[NT];
+#pragma unroll
+    for (uint32_t n = 0; n < NT; ++n) a_row[n] = p.A + static_cast<size_t>(min(8 * n + g, p.M - 1)) * p.lda + 8 * c;
 
     if (lane == 0) {
         for (uint32_t i = 0; i < kRwStages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
@@ -498,12 +506,14 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
         mbar_arrive_expect_tx(bar, kRwBox);
         box_load(smem_u32(boxes) + at * kRwBox, &map_w, bar, k_of(i) / 2, n0);
     };
-    uint4 acts[kChunks];
+    uint4 acts[NT][kChunks];
     const auto load_acts = [&](uint32_t i) {
         if (i >= mine) return;
         const uint32_t k0 = k_of(i), chunks = (p.K - k0) / 32;
 #pragma unroll
-        for (uint32_t ch = 0; ch < kChunks; ++ch) acts[ch] = ch < chunks ? *reinterpret_cast<const uint4*>(a_row + k0 + 32 * ch) : make_uint4(0, 0, 0, 0);
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+            for (uint32_t ch = 0; ch < kChunks; ++ch) acts[n][ch] = ch < chunks ? *reinterpret_cast<const uint4*>(a_row[n] + k0 + 32 * ch) : make_uint4(0, 0, 0, 0);
     };
     // scales and zero points of the tile's row `lane`, a stage ahead
     const bool wide = runs_wide<kGroups>(p, groups);
@@ -523,15 +533,17 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
     if (p.early) grid_dependency_wait();
     load_acts(0);
 
-    float acc[kRwTiles][4] = {};
+    float acc[kRwTiles][NT][4] = {};
 #pragma unroll 1
     for (uint32_t i = 0; i < mine; ++i) {
         const uint32_t at = i % kRwStages;
-        uint4 b[kChunks];
+        uint4 b[NT][kChunks];
         float cs[kGroups];
         uint32_t cz[(kGroups + 3) / 4];
 #pragma unroll
-        for (uint32_t ch = 0; ch < kChunks; ++ch) b[ch] = acts[ch];
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+            for (uint32_t ch = 0; ch < kChunks; ++ch) b[n][ch] = acts[n][ch];
 #pragma unroll
         for (uint32_t q = 0; q < kGroups; ++q) cs[q] = sc[q];
 #pragma unroll
@@ -542,7 +554,7 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
         const uint8_t* const w = boxes + at * kRwBox + g * 128 + 4 * c;
 #pragma unroll
         for (uint32_t q = 0; q < kGroups; ++q) {
-            float part[kRwTiles][4] = {};
+            float part[kRwTiles][NT][4] = {};
             uint32_t z[kRwTiles][2];
 #pragma unroll
             for (uint32_t t = 0; t < kRwTiles; ++t)
@@ -551,16 +563,23 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
                     z[t][r] = __shfl_sync(0xFFFFFFFFu, cz[q / 4] >> (8 * (q % 4)), 16 * t + 8 * r + g) & 0xFFu;
 #pragma unroll
             for (uint32_t ch = q * kGroupChunks; ch < (q + 1) * kGroupChunks; ++ch) {
-                const uint32_t b0 = prmt(b[ch].x, b[ch].z, 0x5410), b1 = prmt(b[ch].x, b[ch].z, 0x7632), b2 = prmt(b[ch].y, b[ch].w, 0x5410),
-                               b3 = prmt(b[ch].y, b[ch].w, 0x7632);
+                uint32_t y[NT][4];
+#pragma unroll
+                for (uint32_t n = 0; n < NT; ++n) {
+                    const uint4 v = b[n][ch];
+                    y[n][0] = prmt(v.x, v.z, 0x5410), y[n][1] = prmt(v.x, v.z, 0x7632), y[n][2] = prmt(v.y, v.w, 0x5410), y[n][3] = prmt(v.y, v.w, 0x7632);
+                }
 #pragma unroll
                 for (uint32_t t = 0; t < kRwTiles; ++t) {
                     uint32_t x[2][4];
 #pragma unroll
                     for (uint32_t r = 0; r < 2; ++r) decode_pairs<F16>(*reinterpret_cast<const uint32_t*>(w + 2048 * t + 1024 * r + ((ch ^ g) << 4)), z[t][r], x[r]);
                     const uint32_t f0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]}, f1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
-                    mma_16816<F16>(part[t], f0, b0, b1);
-                    mma_16816<F16>(part[t], f1, b2, b3);
+#pragma unroll
+                    for (uint32_t n = 0; n < NT; ++n) {
+                        mma_16816<F16>(part[t][n], f0, y[n][0], y[n][1]);
+                        mma_16816<F16>(part[t][n], f1, y[n][2], y[n][3]);
+                    }
                 }
             }
 #pragma unroll
@@ -568,7 +587,10 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
 #pragma unroll
                 for (uint32_t r = 0; r < 2; ++r) {
                     const float f = __shfl_sync(0xFFFFFFFFu, cs[q], 16 * t + 8 * r + g);
-                    acc[t][2 * r] = fmaf(f, part[t][2 * r], acc[t][2 * r]), acc[t][2 * r + 1] = fmaf(f, part[t][2 * r + 1], acc[t][2 * r + 1]);
+#pragma unroll
+                    for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+                        for (uint32_t e = 2 * r; e < 2 * r + 2; ++e) acc[t][n][e] = fmaf(f, part[t][n][e], acc[t][n][e]);
                 }
         }
         // all lanes have read the slot: it may be overwritten
@@ -579,22 +601,24 @@ __global__ void __launch_bounds__(kRwThreads, kRwResident) w4_rows_kernel(const 
 
     // ---- sums of the warps, then of the cluster's CTAs, in order
     __syncthreads();   // every warp is done with its ring, which the sums reuse
-    float* const red = reinterpret_cast<float*>(smem);                       // [warp][8 columns][kRedPitch]
-    float* const sums = red + kRwWarps * 8 * kRwRedPitch;                // [token][kRedPitch]
+    float* const red = reinterpret_cast<float*>(smem);                       // [warp][token][kRwRedPitch]
+    float* const sums = red + kRwWarps * kTok * kRwRedPitch;             // [token][kRwRedPitch]
 #pragma unroll
     for (uint32_t t = 0; t < kRwTiles; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[(warp * 8 + 2 * c + (e & 1)) * kRwRedPitch + 16 * t + 8 * (e >> 1) + g] = acc[t][e];
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[(warp * kTok + 8 * n + 2 * c + (e & 1)) * kRwRedPitch + 16 * t + 8 * (e >> 1) + g] = acc[t][n][e];
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < p.M * kRwRows; i += kRwThreads) {
         const uint32_t m = i / kRwRows, r = i % kRwRows;
         float v = 0.f;
 #pragma unroll
-        for (uint32_t w = 0; w < kRwWarps; ++w) v += red[(w * 8 + m) * kRwRedPitch + r];
+        for (uint32_t w = 0; w < kRwWarps; ++w) v += red[(w * kTok + m) * kRwRedPitch + r];
         if (p.split > 1) sums[m * kRwRedPitch + r] = v;
         else if (n0 + r < p.N) p.C[static_cast<size_t>(m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
     }
-    if (p.split > 1) join_cluster<F16, kRwRows, kRwThreads, 8>(p, sums, rank, 0, p.M, n0);
+    if (p.split > 1) join_cluster<F16, kRwRows, kRwThreads, kTok>(p, sums, rank, 0, p.M, n0);
 }
 
 // --------------------------------------------------------------- more tokens --
@@ -906,13 +930,13 @@ cudaError_t launch_stream(W4Args a, int sms, cudaStream_t s, std::string* err) {
     if (!m.make(a, kSwRows, 128, 0, 0, err)) return cudaErrorInvalidValue;
     return launch_clusters(w4_stream_kernel<F16, MP, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kSwThreads, smem, s);
 }
-template <bool F16, uint32_t G>
+template <bool F16, uint32_t NT, uint32_t G>
 cudaError_t launch_rows(W4Args a, int sms, cudaStream_t s, std::string* err) {
     const uint32_t tiles = (a.N + kRwRows - 1) / kRwRows;
-    a.split = choose_split(tiles, static_cast<uint64_t>(sms) * kRwResident, (a.K + kStageK - 1) / kStageK, kRwWarps);
+    a.split = choose_split(tiles, static_cast<uint64_t>(sms) * RwCfg<NT>::kResident, (a.K + kStageK - 1) / kStageK, kRwWarps);
     Maps m;
     if (!m.make(a, kRwRows, 128, 0, 0, err)) return cudaErrorInvalidValue;
-    return launch_clusters(w4_rows_kernel<F16, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kRwThreads, kRwSmem, s);
+    return launch_clusters(w4_rows_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kRwThreads, RwCfg<NT>::kSmem, s);
 }
 template <bool F16, uint32_t NT, uint32_t G>
 cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
@@ -923,11 +947,19 @@ cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
     if (!m.make(a, kTcRows4, kTcStageK / 2, C::kTok, 64, err)) return cudaErrorInvalidValue;
     return launch_clusters(w4_tc_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kTcThreads4, C::kSmem, s);
 }
+// 9 to 16 tokens in one call of w4_rows_kernel: where its tiles run at once and the product is small.
+// us, rows against tc (BF16, 32-bit scales, zero points, groups of 128): 256x8192 4.4, 9.1; 4096x4096
+// 7.6, 9.1; 6144x4096 10.4, 11.4; 9728x4096 13.5, 17.2; 4096x14336 21.5, 24.1; past the rule 8192x8192
+// 21.6, 20.3; 5120x13824 35.6, 29.7; 12288x4096 (a second round of tiles) 18.9, 17.0.
+bool small_for_rows(const W4Args& a, int sms) {
+    return (a.N + kRwRows - 1) / kRwRows <= static_cast<uint64_t>(sms) * RwCfg<2>::kResident && static_cast<uint64_t>(a.N) * a.K < 1ull << 26;
+}
 template <bool F16, uint32_t G>
 cudaError_t launch_tokens(const W4Args& a, int sms, cudaStream_t s, std::string* err) {
     return a.M == 1    ? launch_stream<F16, 1, G>(a, sms, s, err)
            : a.M == 2  ? launch_stream<F16, 2, G>(a, sms, s, err)
-           : a.M <= 8  ? launch_rows<F16, G>(a, sms, s, err)
+           : a.M <= 8  ? launch_rows<F16, 1, G>(a, sms, s, err)
+           : a.M <= 16 && small_for_rows(a, sms) ? launch_rows<F16, 2, G>(a, sms, s, err)
            : a.M <= 16 ? launch_tc<F16, 16, G>(a, sms, s, err)
                        : launch_tc<F16, 32, G>(a, sms, s, err);
 }

@@ -74,6 +74,12 @@ def test_token_counts_and_ragged_rows(w8, M, N, K, group):
     check(w8, M, N, K, group, "bf16", True, False, seed=M + N, lda_pad=40, ldc_pad=3)
 
 
+@pytest.mark.parametrize("M", [9, 16])
+def test_more_rows_than_tiles_at_once(w8, M):
+    check(w8, M, 9763, 544, 32, "bf16", True, False, seed=M, lda_pad=8, ldc_pad=5)
+    check(w8, M, 9763, 320, 64, "f16", False, True, seed=M)
+
+
 @pytest.mark.parametrize("N,K", [(64, 8192), (256, 28672), (28672, 256), (512, 4096)])
 def test_long_and_wide(w8, N, K):
     for M in (1, 12, 32):
