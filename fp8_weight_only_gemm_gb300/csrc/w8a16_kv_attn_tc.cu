@@ -63,7 +63,7 @@ struct Look {   // a unit, by its 8 groups of 16 keys
     int edge;                          // some rows do not see all keys
 };
 struct Tail {
-    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2][2], odone[2], drain;
+    uint64_t qfull[2], kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2][2], odone[2][2], drain;
     uint64_t lfull[kRing], lempty[kRing];
     uint32_t tmem;
     int abort_flag;
@@ -352,8 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                 mbar_init(smem_u32(&tl->kempty[i]), 1);
                 mbar_init(smem_u32(&tl->vempty[i]), 1);
                 mbar_init(smem_u32(&tl->sfull[i]), 2);   // the products' completion, and the issuer's own arrival
-                for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&tl->pfull[i][k]), 4);
-                mbar_init(smem_u32(&tl->odone[i]), 2);
+                for (int k = 0; k < 2; ++k) {
+                    mbar_init(smem_u32(&tl->pfull[i][k]), 4);
+                    mbar_init(smem_u32(&tl->odone[i][k]), 2);
+                }
             }
             for (uint32_t i = 0; i < kRing; ++i) {
                 mbar_init(smem_u32(&tl->lfull[i]), 1);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                             l *= a;
                             ref = m_new;
                             if (j > 0) {
-                                if (!(ok = wait_warp(smem_u32(&tl->odone[t]), (blocks - 1) & 1, tmo, abort_flag, kWaitO))) break;
+                                if (!(ok = wait_warp(smem_u32(&tl->odone[t][half ^ 1]), ((blocks - 1) >> 1) & 1, tmo, abort_flag, kWaitO))) break;
                                 tc_fence_after();
 #pragma unroll 1
                                 for (uint32_t d = 0; d < DP; d += 8) {
@@ -500,10 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&tl->pfull[t][half]));
                     }
-                    // odone completes once a block. The last S has shown the block two before it done; a
-                    // parity tells one phase from the next only, so the last two are waited for in turn.
-                    ok = ok && wait_warp(smem_u32(&tl->odone[t]), blocks & 1, tmo, abort_flag, kWaitO) &&
-                         wait_warp(smem_u32(&tl->odone[t]), (blocks - 1) & 1, tmo, abort_flag, kWaitO);
+                    // The last unit's products. Each half has a barrier of its own, whose phases are the tile's
+                    // units: a parity tells one phase from the next only, and when both of these products end
+                    // before they are first asked for, the phases of one shared barrier would be taken for others.
+                    const uint32_t last = ((blocks >> 1) - 1) & 1;
+                    ok = ok && wait_warp(smem_u32(&tl->odone[t][0]), last, tmo, abort_flag, kWaitO) &&
+                         wait_warp(smem_u32(&tl->odone[t][1]), last, tmo, abort_flag, kWaitO);
                     if (!ok) break;
                     tc_fence_after();
                     // ---- outputs, or this range's part of them ([d][row], coalesced over rows)
@@ -581,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
 #pragma unroll
                     for (uint32_t k = 0; k < kBlockKeys / 16; ++k)
                         tc_mma_a_tmem(tmu + 2 * kTile + t * DP, tmu + t * kTile + half * kBlockKeys + 8 * k, v0 + k * (2048 >> 4), idO, add || k > 0);
-                    tc_commit(smem_u32(&tl->odone[t]));
-                    mbar_arrive(smem_u32(&tl->odone[t]));
+                    tc_commit(smem_u32(&tl->odone[t][half]));
+                    mbar_arrive(smem_u32(&tl->odone[t][half]));
                 }
             };
             bool ok = true;
