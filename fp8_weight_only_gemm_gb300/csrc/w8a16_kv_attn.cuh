@@ -47,7 +47,9 @@ struct Boundary {
     int32_t first, count;    // the sequence's rows
     uint32_t h, tile;        // the item's head and row tile
 };
-__host__ __device__ constexpr uint64_t boundary_floats(uint32_t ctas) { return (ctas * sizeof(Boundary) + 15) / 16 * 4; }
+// After them, `parts` alone (a multiple of 4 of them, and where the slots begin).
+__host__ __device__ constexpr uint64_t parts_at(uint32_t ctas) { return (ctas * sizeof(Boundary) + 15) / 16 * 4; }
+__host__ __device__ constexpr uint64_t boundary_floats(uint32_t ctas) { return parts_at(ctas) + (ctas + 3) / 4 * 4; }
 __device__ __forceinline__ void write_boundary(float* ws, uint64_t u0, uint64_t item_first, uint32_t item_units, const Seq& s,
                                                uint32_t h, uint32_t tile, uint64_t total, uint64_t ctas) {
     Boundary b{0, 0, s.first, s.count, h, tile};
@@ -60,6 +62,7 @@ __device__ __forceinline__ void write_boundary(float* ws, uint64_t u0, uint64_t 
         }
     }
     reinterpret_cast<Boundary*>(ws)[c] = b;
+    reinterpret_cast<uint32_t*>(ws + parts_at(gridDim.x))[c] = b.parts;
 }
 
 // Zeros in the rows of sequences without keys.

@@ -374,8 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // A dependent that also wants TMEM may be scheduled from here on: this CTA holds its own.
-    grid_launch_dependents();
     const uint32_t tm = tl->tmem;
 
     const uint64_t total = total_units<kWarpsAll>(p, sh_units, blockIdx.x == 0);
@@ -782,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     __syncthreads();
     tc_fence_after();
     if (warp == kIssueWarp) tmem_dealloc(tm, 512);
+    grid_launch_dependents();   // late: the join's blocks beside working CTAs cost them 7 % (160 us against 149)
 }
 
 // Joins the parts of split items in key order: a block per boundary between CTAs' ranges and
