@@ -583,52 +583,14 @@ __device__ __forceinline__ void load_dims(const float* from, float (&x)[V]) {
 // of 1000, whose items have 2, 78 for 70. 8 warps a row: 79 there.)
 template <bool F16, uint32_t DP>
 __global__ void __launch_bounds__(kThreads) kv_attn_join_kernel(const AttnArgs p) {
-    __shared__ uint32_t sh_count[kWarps];
-    __shared__ uint32_t sh_c;
     __shared__ float sh_m[kWarps], sh_l[kWarps];
     __shared__ __align__(16) float sh_acc[kWarps][DP];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
-    if (threadIdx.x == 0) sh_c = 0;
     grid_dependency_wait();
     grid_launch_dependents();
-    // ---- the k-th boundary with parts; a thread looks at 4
-    const Boundary* const bounds = reinterpret_cast<const Boundary*>(p.ws);
-    const uint32_t* const parts = reinterpret_cast<const uint32_t*>(p.ws + parts_at(p.ctas));
-    uint32_t k = blockIdx.x;
-    for (uint32_t base = 0; base < p.ctas; base += 4 * kThreads) {
-        const uint32_t c0 = base + 4 * threadIdx.x;
-        uint32_t has = 0;
-        if (c0 < p.ctas) {   // (past the last one: whatever is there is masked; CTA 0 begins no item inside)
-            const uint4 v = *reinterpret_cast<const uint4*>(parts + c0);
-            has = ((v.x ? 1u : 0u) | (v.y ? 2u : 0u) | (v.z ? 4u : 0u) | (v.w ? 8u : 0u)) & (p.ctas - c0 < 4 ? (1u << (p.ctas - c0)) - 1u : 15u);
-        }
-        uint32_t before = __popc(has);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, o);
-            if (lane >= static_cast<uint32_t>(o)) before += x;
-        }
-        __syncthreads();
-        if (lane == 31) sh_count[warp] = before;
-        before -= __popc(has);
-        __syncthreads();
-        uint32_t all = 0;
-#pragma unroll
-        for (uint32_t w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sh_count[w];
-            all += sh_count[w];
-        }
-        if (k >= before && k < before + __popc(has)) {
-            for (uint32_t i = k - before; i; --i) has &= has - 1;
-            sh_c = c0 + __ffs(has) - 1;
-        }
-        if (k < all) break;
-        k -= all;
-    }
-    __syncthreads();
-    const uint32_t c = sh_c;
+    const uint32_t c = split_boundary<kThreads>(p, blockIdx.x);
     if (c == 0) return;   // fewer items are split
-    const Boundary b = bounds[c];
+    const Boundary b = reinterpret_cast<const Boundary*>(p.ws)[c];
     const uint32_t row = b.tile * p.tile_rows + r;
     if (row >= static_cast<uint32_t>(b.count) * p.group) return;
     const float* const slots = p.ws + boundary_floats(p.ctas);

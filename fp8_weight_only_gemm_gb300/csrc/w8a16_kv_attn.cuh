@@ -65,6 +65,49 @@ __device__ __forceinline__ void write_boundary(float* ws, uint64_t u0, uint64_t 
     reinterpret_cast<uint32_t*>(ws + parts_at(gridDim.x))[c] = b.parts;
 }
 
+// The CTA of the k-th boundary with parts (from 0), or 0 if there are fewer; for all of a block. A thread looks at 4.
+template <uint32_t THREADS>
+__device__ __forceinline__ uint32_t split_boundary(const AttnArgs& p, uint32_t k) {
+    __shared__ uint32_t sh_count[THREADS / 32];
+    __shared__ uint32_t sh_c;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t* const parts = reinterpret_cast<const uint32_t*>(p.ws + parts_at(p.ctas));
+    if (threadIdx.x == 0) sh_c = 0;
+    for (uint32_t base = 0; base < p.ctas; base += 4 * THREADS) {
+        const uint32_t c0 = base + 4 * threadIdx.x;
+        uint32_t has = 0;
+        if (c0 < p.ctas) {   // (past the last one: whatever is there is masked; CTA 0 begins no item inside)
+            const uint4 v = *reinterpret_cast<const uint4*>(parts + c0);
+            has = ((v.x ? 1u : 0u) | (v.y ? 2u : 0u) | (v.z ? 4u : 0u) | (v.w ? 8u : 0u)) & (p.ctas - c0 < 4 ? (1u << (p.ctas - c0)) - 1u : 15u);
+        }
+        const uint32_t n = __popc(has);
+        uint32_t before = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (lane >= static_cast<uint32_t>(o)) before += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh_count[warp] = before;
+        before -= n;
+        __syncthreads();
+        uint32_t all = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += sh_count[w];
+            all += sh_count[w];
+        }
+        if (k >= before && k < before + n) {
+            for (uint32_t i = k - before; i; --i) has &= has - 1;
+            sh_c = c0 + __ffs(has) - 1;
+        }
+        if (k < all) break;
+        k -= all;
+    }
+    __syncthreads();
+    return sh_c;
+}
+
 // Zeros in the rows of sequences without keys.
 __device__ __forceinline__ void zero_keyless(const AttnArgs& p) {
     for (uint32_t b = blockIdx.x; b < p.b.batch; b += gridDim.x) {

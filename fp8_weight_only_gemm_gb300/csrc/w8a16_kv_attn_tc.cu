@@ -783,39 +783,85 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     grid_launch_dependents();   // late: the join's blocks beside working CTAs cost them 7 % (160 us against 149)
 }
 
-// Joins the parts of split items in key order: a block per boundary between CTAs' ranges and
-// 16 dims, a thread per row.
+// Joins the parts of split items, in an order that their number and the rows' alone decide: a block
+// for the k-th split item and 16 dims, a thread a row; where there are 128 rows or fewer, 256 /
+// rows threads take a row's parts in turn. Two parts are in flight at a time.
 constexpr uint32_t kJoinThreads = kItemRows, kJoinDims = 16;
 template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) kv_attn_tc_join_kernel(const AttnArgs p, uint32_t dp) {
+__global__ void __launch_bounds__(kJoinThreads, 4) kv_attn_tc_join_kernel(const AttnArgs p, uint32_t dp) {
+    __shared__ float sh_m[kJoinThreads], sh_l[kJoinThreads], sh_acc[kJoinDims][kJoinThreads];
     grid_dependency_wait();
-    grid_launch_dependents();
-    const uint32_t c = blockIdx.x + 1, d0 = blockIdx.y * kJoinDims;
+    // (a block for each boundary where most have parts; elsewhere one for each item)
+    const uint32_t c = gridDim.x == p.ctas - 1 ? blockIdx.x + 1 : split_boundary<kJoinThreads>(p, blockIdx.x), d0 = blockIdx.y * kJoinDims;
     const Boundary b = reinterpret_cast<const Boundary*>(p.ws)[c];
-    const uint32_t row = threadIdx.x, r = b.tile * kItemRows + row;
-    if (b.parts == 0 || r >= static_cast<uint32_t>(b.count) * p.group) return;
+    if (b.parts == 0) return;   // (of CTA 0 too: fewer items are split)
+    const uint32_t rows = min(static_cast<uint32_t>(b.count) * p.group - b.tile * kItemRows, kItemRows);
+    const uint32_t lanes = rows <= 32 ? 32u : rows <= 64 ? 64u : rows <= 128 ? 128u : 256u, turns = kJoinThreads / lanes;
+    const uint32_t row = threadIdx.x % lanes, turn = threadIdx.x / lanes;
     const uint64_t stride = static_cast<uint64_t>(dp + 2) * kItemRows;
     const float* const slots = p.ws + boundary_floats(p.ctas);
-    const auto slot = [&](uint32_t i) { return slots + (i == 0 ? b.slot : 2ull * (c + i - 1)) * stride; };
-    float m = -INFINITY;
-    for (uint32_t i = 0; i < b.parts; ++i) m = fmaxf(m, slot(i)[dp * kItemRows + row]);
-    float acc[kJoinDims] = {}, l = 0.f;
-    for (uint32_t i = 0; i < b.parts; ++i) {
-        const float* s = slot(i);
-        const float mi = s[dp * kItemRows + row];
-        const float a = mi == -INFINITY ? 0.f : ex2(mi - m);
-        l = fmaf(a, s[(dp + 1) * kItemRows + row], l);
+    constexpr uint32_t kAtOnce = 2;
+    float m = -INFINITY, l = 0.f, acc[kJoinDims] = {};
+    for (uint32_t i0 = turn; i0 < b.parts; i0 += turns * kAtOnce) {
+        float x[kAtOnce][kJoinDims], mi[kAtOnce], li[kAtOnce];
 #pragma unroll
-        for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] = fmaf(a, s[(d0 + d) * kItemRows + row], acc[d]);
+        for (uint32_t j = 0; j < kAtOnce; ++j) {
+            const uint32_t i = i0 + turns * j;
+            mi[j] = -INFINITY, li[j] = 0.f;
+#pragma unroll
+            for (uint32_t d = 0; d < kJoinDims; ++d) x[j][d] = 0.f;
+            if (i < b.parts && row < rows) {
+                const float* const s = slots + (i == 0 ? b.slot : 2ull * (c + i - 1)) * stride + row;
+                mi[j] = s[dp * kItemRows], li[j] = s[(dp + 1) * kItemRows];
+#pragma unroll
+                for (uint32_t d = 0; d < kJoinDims; ++d) x[j][d] = s[(d0 + d) * kItemRows];
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (uint32_t j = 0; j < kAtOnce; ++j) top = fmaxf(top, mi[j]);
+        const float keep = m == -INFINITY ? 0.f : ex2(m - top);
+        l *= keep;
+#pragma unroll
+        for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] *= keep;
+        m = top;
+#pragma unroll
+        for (uint32_t j = 0; j < kAtOnce; ++j) {
+            const float a = mi[j] == -INFINITY ? 0.f : ex2(mi[j] - m);   // (0 times NaN: a query that is not finite)
+            l = fmaf(a, li[j], l);
+#pragma unroll
+            for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] = fmaf(a, x[j][d], acc[d]);
+        }
     }
+    if (turns > 1) {
+        sh_m[threadIdx.x] = m, sh_l[threadIdx.x] = l;
+#pragma unroll
+        for (uint32_t d = 0; d < kJoinDims; ++d) sh_acc[d][threadIdx.x] = acc[d];
+        __syncthreads();
+        if (turn > 0) return;
+        float top = m;
+        for (uint32_t t = 1; t < turns; ++t) top = fmaxf(top, sh_m[t * lanes + row]);
+        const float keep = m == -INFINITY ? 0.f : ex2(m - top);
+        l *= keep;
+#pragma unroll
+        for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] *= keep;
+        for (uint32_t t = 1; t < turns; ++t) {
+            const uint32_t at = t * lanes + row;
+            const float a = sh_m[at] == -INFINITY ? 0.f : ex2(sh_m[at] - top);
+            l = fmaf(a, sh_l[at], l);
+#pragma unroll
+            for (uint32_t d = 0; d < kJoinDims; ++d) acc[d] = fmaf(a, sh_acc[d][at], acc[d]);
+        }
+    }
+    if (row >= rows) return;
+    const uint32_t r = b.tile * kItemRows + row;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(b.first + static_cast<int>(r / p.group)) * p.out.token_stride +
                     static_cast<int64_t>(b.h * p.group + r % p.group) * p.out.head_stride + d0;
-    uint32_t w[kJoinDims / 2];
 #pragma unroll
-    for (uint32_t d = 0; d < kJoinDims / 2; ++d) w[d] = pack2<F16>(acc[2 * d] * inv, acc[2 * d + 1] * inv);
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (uint32_t d = 0; d < kJoinDims; d += 8)
+        *reinterpret_cast<uint4*>(dst + d) = make_uint4(pack2<F16>(acc[d] * inv, acc[d + 1] * inv), pack2<F16>(acc[d + 2] * inv, acc[d + 3] * inv),
+                                                        pack2<F16>(acc[d + 4] * inv, acc[d + 5] * inv), pack2<F16>(acc[d + 6] * inv, acc[d + 7] * inv));
 }
 
 template <bool F16, uint32_t DP>
@@ -835,7 +881,8 @@ cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kv_attn_tc_kernel<F16, DP>, p);
     if (e != cudaSuccess || p.ctas < 2) return e;
-    cfg.gridDim = dim3(p.ctas - 1, (p.c.head_dim + kJoinDims - 1) / kJoinDims, 1);
+    const uint64_t items = static_cast<uint64_t>(p.b.batch) * p.c.kv_heads * ((static_cast<uint64_t>(p.b.max_q) * p.group + kItemRows - 1) / kItemRows);
+    cfg.gridDim = dim3(static_cast<uint32_t>(items < p.ctas ? items : p.ctas - 1), p.c.head_dim / kJoinDims, 1);   // no more are split
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv_attn_tc_join_kernel<F16>, p, DP);
@@ -843,8 +890,14 @@ cudaError_t launch(const AttnArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-// Heads above 128 leave no room in TMEM for two row tiles' outputs.
-bool kv_attn_tc_applies(uint32_t head_dim, uint32_t rows_per_head) { return head_dim <= 128 && rows_per_head >= 64; }
+// Heads above 128 leave no room in TMEM for two row tiles' outputs. Rows: this kernel's time hardly
+// depends on them up to 128, the other's goes with tiles of 16. us, that one against this one, 8 heads of 128:
+//                             20 rows      32          40          64          128
+//     1 sequence of 1000     12.7 16.8  12.9 16.9   13.0 17.2   14.3 17.3   20.3 18.7
+//     1 of 16000             30.0 35.1  30.7 35.3   33.0 36.3   44.2 36.6   70.2 40.7
+//     16 of 2000             50.2 62.2  52.7 62.5   68.6 62.6   89.8 63.2    150 65.7
+//     32 of 8000              243  243   248  245    353  245    466  247    898  250
+bool kv_attn_tc_applies(uint32_t head_dim, uint32_t rows_per_head) { return head_dim <= 128 && rows_per_head > 32; }
 
 uint64_t kv_attn_tc_ws_bytes(uint32_t head_dim, int sms) {
     return 4 * boundary_floats(static_cast<uint32_t>(sms)) + 8ull * static_cast<uint32_t>(sms) * ((head_dim <= 64 ? 64u : 128u) + 2) * kItemRows;
