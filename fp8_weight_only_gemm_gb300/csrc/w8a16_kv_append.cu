@@ -13,10 +13,14 @@
 // maximum over the item's new tokens, pass 2 rotates again and encodes. A thread
 // holds two 8-element chunks of a token (the two halves of eight rotary pairs in
 // the half layout, 16 consecutive elements in the interleaved one), so every load is
-// 16 bytes, every store 8 or 16. Queries are independent 16-element tasks, in blocks of
-// their own behind the items'. Single tokens take a warp per item (8 lanes hold a
-// 128-element head: the launch is bound by its two dependent loads, length -> page ->
-// codes), longer chunks a 128-thread block per item.
+// 16 bytes, every store 8 or 16. Queries are independent tasks of 16 elements, in blocks of
+// their own behind the items', two a thread.
+//
+// Bound by: a few tokens, by two dependent loads behind the launch, length -> page -> codes (48
+// sequences, one token: 2.8 us device time); prompts by HBM, where 28 us for 138 MB (4 sequences of 1501
+// tokens, 64 query heads) are 4.9 TB/s. A thread's query elements are asked for before the token's
+// position is known: with one task a thread, found by 64-bit divisions, and asked for after it,
+// that took 33 us; four tasks a thread take 31.6.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -29,7 +33,7 @@ namespace {
 
 __device__ DeviceStatus g_kv_append_status;
 
-constexpr uint32_t kThreads = 128;
+constexpr uint32_t kThreads = 128, kQueryTasks = 2;
 constexpr int kMinScaleExp = -60;
 
 struct AppendArgs {
@@ -40,6 +44,7 @@ struct AppendArgs {
     uint32_t pages_per_seq;   // most pages that one sequence's new tokens touch
     uint32_t items;           // batch * pages_per_seq * kv_heads * 2
     uint32_t item_blocks;
+    uint32_t token_blocks;    // of a token's queries
 };
 
 // The smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8), at least 2^-60.
@@ -86,12 +91,10 @@ __device__ __forceinline__ void rotate(float& lo, float& hi, float c, float s) {
     hi = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-// The 16 values of a task, rotated for `pos`.
+// The 16 values of a task, from its chunks' words, rotated for `pos`.
 template <bool F16>
-__device__ __forceinline__ void load_rotated(const uint16_t* head, const w8a16_rope_t& r, const Chunks& ch, uint32_t i,
-                                             int pos, float (&x)[16]) {
-    const uint4 qa = *reinterpret_cast<const uint4*>(head + ch.a);
-    const uint4 qb = *reinterpret_cast<const uint4*>(head + ch.b);
+__device__ __forceinline__ void rotated(const uint4& qa, const uint4& qb, const w8a16_rope_t& r, const Chunks& ch, uint32_t i, int pos,
+                                        float (&x)[16]) {
     const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -115,36 +118,52 @@ __device__ __forceinline__ void load_rotated(const uint16_t* head, const w8a16_r
         for (int e = 0; e < 8; ++e) rotate(x[e], x[8 + e], c[e], s[e]);
     }
 }
-
-// 16 elements of one query head.
 template <bool F16>
-__device__ void rotate_query(const AppendArgs& p, uint64_t task) {
-    const uint32_t per_head = p.c.head_dim / 16;
-    const uint32_t i = static_cast<uint32_t>(task % per_head);
-    const uint64_t th = task / per_head;
-    const uint32_t h = static_cast<uint32_t>(th % p.q.heads), n = static_cast<uint32_t>(th / p.q.heads);
-    const uint32_t b = seq_of_row(p.b, n);
-    const Seq seq = sequence(p.b, p.c.page_size, b);
+__device__ __forceinline__ void load_rotated(const uint16_t* head, const w8a16_rope_t& r, const Chunks& ch, uint32_t i,
+                                             int pos, float (&x)[16]) {
+    rotated<F16>(*reinterpret_cast<const uint4*>(head + ch.a), *reinterpret_cast<const uint4*>(head + ch.b), r, ch, i, pos, x);
+}
+
+// Up to kQueryTasks tasks (16 elements of a query head) of token n a thread, `first` and every
+// kThreads-th after it; they are asked for before the token's position is known.
+template <bool F16>
+__device__ __forceinline__ void rotate_queries(const AppendArgs& p, uint32_t n, uint32_t first) {
+    const uint32_t per_head = p.c.head_dim / 16, tasks = p.q.heads * per_head;
+    const uint16_t* const src = static_cast<const uint16_t*>(p.q.ptr) + static_cast<int64_t>(n) * p.q.token_stride;
+    uint16_t* const dst = static_cast<uint16_t*>(p.q_out.ptr) + static_cast<int64_t>(n) * p.q_out.token_stride;
+    uint4 qa[kQueryTasks], qb[kQueryTasks];
+    Chunks ch[kQueryTasks];
+    uint32_t h[kQueryTasks], i[kQueryTasks];
+#pragma unroll
+    for (uint32_t u = 0; u < kQueryTasks; ++u) {
+        const uint32_t task = first + u * kThreads;
+        h[u] = task / per_head, i[u] = task % per_head;
+        ch[u] = chunks_of(p.rope.rotary_dim, p.rope.interleaved, i[u]);
+        if (task >= tasks) continue;
+        const uint16_t* const head = src + static_cast<int64_t>(h[u]) * p.q.head_stride;
+        qa[u] = *reinterpret_cast<const uint4*>(head + ch[u].a), qb[u] = *reinterpret_cast<const uint4*>(head + ch[u].b);
+    }
+    const Seq seq = sequence(p.b, p.c.page_size, seq_of_row(p.b, n));
     const int t = static_cast<int>(n) - seq.first;
     if (t < 0 || t >= seq.count) return;   // rows that no sequence claims (a bad one: reported by its items)
     const int pos = seq.len - seq.count + t;
-    Chunks ch = chunks_of(p.rope.rotary_dim, p.rope.interleaved, i);
-    if (pos < 0) ch.rotated = false;   // padding: passed through
-    if (ch.rotated && pos >= static_cast<int>(p.rope.rows)) {
-        record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pos));
-        return;
-    }
-    const uint16_t* src = static_cast<const uint16_t*>(p.q.ptr) + static_cast<int64_t>(n) * p.q.token_stride +
-                          static_cast<int64_t>(h) * p.q.head_stride;
-    uint16_t* dst = static_cast<uint16_t*>(p.q_out.ptr) + static_cast<int64_t>(n) * p.q_out.token_stride +
-                    static_cast<int64_t>(h) * p.q_out.head_stride;
-    float x[16];
-    load_rotated<F16>(src, p.rope, ch, i, pos, x);
-    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = pack2<F16>(x[2 * e], x[2 * e + 1]);
-    *reinterpret_cast<uint4*>(dst + ch.a) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(dst + ch.b) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (uint32_t u = 0; u < kQueryTasks; ++u) {
+        if (first + u * kThreads >= tasks) break;
+        if (pos < 0) ch[u].rotated = false;   // padding: passed through
+        if (ch[u].rotated && pos >= static_cast<int>(p.rope.rows)) {
+            record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pos));
+            continue;
+        }
+        float x[16];
+        rotated<F16>(qa[u], qb[u], p.rope, ch[u], i[u], pos, x);
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack2<F16>(x[2 * e], x[2 * e + 1]);
+        uint16_t* const head = dst + static_cast<int64_t>(h[u]) * p.q_out.head_stride;
+        *reinterpret_cast<uint4*>(head + ch[u].a) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(head + ch[u].b) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // TPI threads per item: 32 (a warp, kThreads / 32 items a block) or kThreads.
@@ -154,10 +173,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
     grid_dependency_wait();     // k, v, q and the cache may be the previous kernel's
     grid_launch_dependents();
     if (blockIdx.x >= p.item_blocks) {
-        const uint64_t tasks = static_cast<uint64_t>(p.b.tokens) * p.q.heads * (p.c.head_dim / 16);
-        const uint64_t step = static_cast<uint64_t>(gridDim.x - p.item_blocks) * kThreads;
-        for (uint64_t t = static_cast<uint64_t>(blockIdx.x - p.item_blocks) * kThreads + threadIdx.x; t < tasks; t += step)
-            rotate_query<F16>(p, t);
+        const uint32_t at = blockIdx.x - p.item_blocks;
+        rotate_queries<F16>(p, at / p.token_blocks, at % p.token_blocks * (kThreads * kQueryTasks) + threadIdx.x);
         return;
     }
     const uint32_t lane = threadIdx.x % TPI;
@@ -262,14 +279,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
 int launch_kv_append(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_t act_dtype, const w8a16_heads_t& k,
                      const w8a16_heads_t& v, const w8a16_heads_t& q, const w8a16_heads_t& q_out,
                      const w8a16_rope_t& rope, cudaStream_t s, std::string* err) {
-    AppendArgs p{c, b, k, v, q, q_out, rope, 0, 0, 0};
+    AppendArgs p{c, b, k, v, q, q_out, rope, 0, 0, 0, 0};
     p.pages_per_seq = (b.max_q + c.page_size - 2) / c.page_size + 1;
     const uint64_t items = 2ull * b.batch * p.pages_per_seq * c.kv_heads;
-    // a block per item where a page takes more tasks than a warp has lanes twice over
-    const bool wide = static_cast<uint64_t>(b.max_q < c.page_size ? b.max_q : c.page_size) * (c.head_dim / 16) > 64;
+    // A warp per item where a page's new tokens have a task a lane at most, else a block. us, warp against
+    // block (8 heads of 128, 32 query heads): 48 sequences of 1 token (8 tasks) 2.8 3.2; 1 of 5 (40) 3.5
+    // 2.7; 48 of 5 4.5 4.2; 1 of 8 3.5 2.8; 32 of 16 7.6 4.3; 4 of 1500 41.9 27.9.
+    const bool wide = static_cast<uint64_t>(b.max_q < c.page_size ? b.max_q : c.page_size) * (c.head_dim / 16) > 32;
     const uint64_t item_blocks = wide ? items : (items + kThreads / 32 - 1) / (kThreads / 32);
-    const uint64_t q_tasks = q.ptr ? static_cast<uint64_t>(b.tokens) * q.heads * (c.head_dim / 16) : 0;
-    const uint64_t q_blocks = (q_tasks + kThreads - 1) / kThreads;
+    p.token_blocks = (q.heads * (c.head_dim / 16) + kThreads * kQueryTasks - 1) / (kThreads * kQueryTasks);
+    const uint64_t q_blocks = q.ptr ? static_cast<uint64_t>(b.tokens) * p.token_blocks : 0;
     if (items > 0x7FFFFFFFull || item_blocks + q_blocks > 0x7FFFFFFFull) {
         *err = "cache append: too many pages or queries for one launch";
         return W8A16_ERR_RANGE;
