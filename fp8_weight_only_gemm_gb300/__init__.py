@@ -4,7 +4,10 @@ C[M, N] (BF16) = A[M, K] (BF16, any row pitch) x dequant(W[N, K] FP8 E4M3, one F
 scale per 128x128 block)^T, computed by hand-written tcgen05/TMA kernels in
 ``libw8a16.so`` behind a C ABI (include/w8a16.h). This package is the thin
 Python binding: torch provides device memory and streams only. The library also
-holds the weight block quantiser that produces W and the block scales.
+holds the weight block quantiser that produces W and the block scales, and what a
+decoder's attention block needs next to its projections: an 8-bit paged key/value cache
+(KVCache, kv_append with rotary positions, kv_attention) and a product with 4-bit weights
+and group scales (gemm_w4). examples/attention_block.py runs them together.
 """
 from .binding import (FLAG_PDL, Plan, VARIANT_AUTO, VARIANT_SIMT, VARIANT_TC, VARIANT_TC8, VARIANT_W8A8,
                       VARIANT_PRESPLIT, WEIGHTS_BF16, WEIGHTS_F32, W8A16Error,
