@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kern
 // with the decoded weights in TMEM as A (lane = weight row, column j = values 2 j and 2 j + 1)
 // and the activations, as TMA wrote them, as B. Warps 0-3 decode, a thread a row, and add
 // scale * D to the row's sums; warp 4 copies and issues. Two slots of TMEM: while a chunk's
-// product runs the next one is decoded, and a slot is free again once its sums have been read.
+// product runs the next one is decoded, and a slot is free again once its sums have been read. The
+// two chunks of a group of 128 add to one D, which is read once.
 constexpr uint32_t kTcThreads4 = 160, kTcRows4 = 128, kTcStageK = 128, kTcWBytes = kTcRows4 * kTcStageK / 2, kTcResident = 4;
 constexpr uint32_t kTcTmemCols = 128, kTcRedPitch = kTcRows4 + 4;
 template <uint32_t NT, uint32_t G>
@@ -636,12 +637,12 @@ struct TcCfg {
     static constexpr uint32_t kTok = NT;                                  // the product's columns
     static constexpr uint32_t kCk = G < 64 ? G : 64, kPerStage = kTcStageK / kCk, kACols = kCk / 2;
     static constexpr uint32_t kStageGroups = kTcStageK / G;
-    static constexpr uint32_t kSlotCols = kACols + kTok;
+    static constexpr bool kWhole = G == kTcStageK;                        // a stage is a group: its chunks share a product
     static constexpr uint32_t kActBytes = kTok * 128;                       // 64 values of K
     static constexpr uint32_t kStageBytes = kTcWBytes + 2 * kActBytes;
     static constexpr uint32_t kStages = NT > 16 ? 3 : 4;
     static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes;
-    static_assert(2 * kSlotCols <= kTcTmemCols && kPerStage % 2 == 0, "slots");
+    static_assert(2 * (kACols + kTok) <= kTcTmemCols && kPerStage % 2 == 0 && (!kWhole || kPerStage == 2), "slots");
     static_assert(kTok * kTcRedPitch * 4 <= kStages * kStageBytes, "the sums reuse the ring");
     static_assert(kTcResident * (kSmem + 2048) <= 228 * 1024, "CTAs of an SM");
 };
@@ -746,10 +747,10 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
                 tc_fence_after();
                 const uint32_t k = j * C::kCk;
                 const uint64_t b = desc + at * (C::kStageBytes >> 4) + ((k / 64 * C::kActBytes + k % 64 * 2) >> 4);
-                const uint32_t tA = tmu + slot * C::kSlotCols, tD = tA + C::kACols;
+                const uint32_t tA = tmu + slot * C::kACols, tD = tmu + 2 * C::kACols + (C::kWhole ? s & 1 : slot) * C::kTok;
                 if (elected) {
 #pragma unroll
-                    for (uint32_t e = 0; e < C::kCk / 16; ++e) tc_mma_a_tmem(tD, tA + 8 * e, b + 2 * e, kIdesc, e ? 1u : 0u);
+                    for (uint32_t e = 0; e < C::kCk / 16; ++e) tc_mma_a_tmem(tD, tA + 8 * e, b + 2 * e, kIdesc, e || (C::kWhole && j) ? 1u : 0u);
                     tc_commit(smem_u32(&d_full[slot]));
                 }
                 __syncwarp();
@@ -791,18 +792,18 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
             zp = z[0];
         };
         load_params(0);
-        float f[2] = {};   // scales of the slots' chunks
+        float f[2] = {};   // scales of the products in flight
         const auto done = [&](uint32_t i, uint32_t slot) {   // the product of chunk i, in this slot
             const bool ok = wait_warp(smem_u32(&d_full[slot]), (i >> 1) & 1, p.timeout_ns, &abort_flag);
             tc_fence_after();
             return ok;
         };
-        const auto fold = [&](uint32_t slot) {   // sums += scale * D
-            const uint64_t ff = pack_f32x2(f[slot], f[slot]);
+        const auto fold = [&](uint32_t slot, float scale) {   // sums += scale * D
+            const uint64_t ff = pack_f32x2(scale, scale);
 #pragma unroll
             for (uint32_t t = 0; t < C::kTok; t += 16) {
                 float d[2][8];
-                const uint32_t tD = tm + slot * C::kSlotCols + C::kACols + lanes + t;
+                const uint32_t tD = tm + 2 * C::kACols + slot * C::kTok + lanes + t;
                 tmem_ld_32x32b_x8(tD, d[0]);
                 tmem_ld_32x32b_x8(tD + 8, d[1]);
                 tc_wait_ld();
@@ -828,8 +829,9 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
                 uint4 v = *reinterpret_cast<const uint4*>(w + (((j * C::kCk / 32) ^ (row >> 1 & 3)) << 4));
                 if (i >= 2) ok = ok && done(i - 2, slot);
                 if (!ok) break;
-                if (i >= 2) fold(slot);
-                const uint32_t tA = tm + slot * C::kSlotCols + lanes;
+                if (!C::kWhole && i >= 2) fold(slot, f[slot]);
+                if (C::kWhole && j == 1 && s > 0) fold(s & 1 ^ 1, f[0]);
+                const uint32_t tA = tm + slot * C::kACols + lanes;
 #pragma unroll
                 for (uint32_t h = 0; h < C::kCk / 32; ++h) {
                     if (h > 0) v = *reinterpret_cast<const uint4*>(w + (((j * C::kCk / 32 + h) ^ (row >> 1 & 3)) << 4));
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
                     decode_row8<F16>(v.w, cz[q], o + 12);
                     tmem_st_32x32b_x16(tA + 16 * h, o);
                 }
-                f[slot] = cs[q];
+                if (!C::kWhole || j == 1) f[C::kWhole ? 0 : slot] = cs[q];
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -850,9 +852,9 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
         if (n_stages > 0) {   // the last two chunks
             const uint32_t n = n_stages * C::kPerStage;
             ok = ok && done(n - 2, 0);
-            if (ok) fold(0);
+            if (!C::kWhole && ok) fold(0, f[0]);
             ok = ok && done(n - 1, 1);
-            if (ok) fold(1);
+            if (ok) fold(C::kWhole ? n_stages & 1 ^ 1 : 1, f[C::kWhole ? 0 : 1]);
         }
     }
 
