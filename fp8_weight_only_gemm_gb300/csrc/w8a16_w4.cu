@@ -32,18 +32,19 @@
 // Where the steps are (us, BF16, 32-bit scales, zero points, groups of 128):
 //                        1024x4096   4096x4096   12288x4096   28672x8192   (N x K)
 //     2 tokens  stream      3.1         5.4         10.4         32.7
-//               rows        3.6         6.5         13.2         37.5
-//     8 tokens  rows        3.8         7.1         13.7         40.5
-//               tc          5.8         8.1         16.3         57.1
-//     16        rows        4.4         7.6         18.9         59.0
-//               tc          6.3         9.1         17.0         58.7
+//               rows        3.5         6.7         13.3         37.1
+//     8 tokens  rows        3.8         7.1         13.8         40.4
+//               tc          6.1         8.7         18.0         46.3
+//     16        rows        4.4         7.5         18.9         59.4
+//               tc          6.4         9.1         18.2         47.4
 // (12288 rows are 1.3 rounds of tiles there.)
 // Bound by: the stream of bytes at large sizes (28672x8192, one token: 132 MB in 33 us, 4.1 TB/s with groups
-// of 32), the time to the first bytes and the join at small ones. What counts for it is bytes in
-// flight: rings of 192 KB an SM without a barrier between warps stream twice as fast as rings of 96
-// KB behind a CTA's barriers did. With 9 tokens and more, decoding, the products' hand-over and the
-// folding take turns (14336x5120, 32 tokens: 22 us; 17.8 without the decoding, 19.1 without the
-// folding, 10.1 with neither products nor join).
+// of 32, 4.6 with groups of 128), the time to the first bytes and the join at small ones. What
+// counts for it is bytes in flight: rings of 192 KB an SM without a barrier between warps stream
+// twice as fast as rings of 96 KB behind a CTA's barriers did. With more tokens (14336x5120, 32
+// tokens: 21.7 us) decoding, the products' hand-over and the folding take turns: a copy of the
+// kernel took 4.5 us less without the decoding, 2.2 without the join, 10 in all with neither these
+// nor products.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kern
     }
 
     // Dependents come in only now: on the SMs whose CTAs were done first they took part of what the rest
-    // runs on (12288x4096, 8 tokens, call behind call: 12.9 us against 11.5).
+    // runs on (12288x4096, 8 tokens, call behind call: 12.9 us against 11.2).
     grid_launch_dependents();
     // ---- sums of the warps, then of the cluster's CTAs, in order
     __syncthreads();   // every warp is done with its ring, which the sums reuse
@@ -863,7 +864,9 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
     __syncthreads();   // products and copies are done: the sums reuse the ring, and TMEM goes back before any wait for a peer
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tm, kTcTmemCols);
-    // (Dependents come in as CTAs end: let in here or at the start they cost 14336x5120, 32 tokens, 0.7 us of 22.4.)
+    // Dependents come in here (every CTA has had its TMEM): let in at the start they take the places of CTAs that
+    // are done (28672x8192, 32 tokens: 60 us for 50), not before the end 12288x4096 takes 20 for 18.
+    grid_launch_dependents();
     float* const red = reinterpret_cast<float*>(smem);   // [token][kTcRedPitch]
     if (warp < 4) {
 #pragma unroll
@@ -951,9 +954,9 @@ cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
     return launch_clusters(w4_tc_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kTcThreads4, C::kSmem, s);
 }
 // 9 to 16 tokens in one call of w4_rows_kernel: where its tiles run at once and the product is small.
-// us, rows against tc (BF16, 32-bit scales, zero points, groups of 128): 256x8192 4.4, 9.1; 4096x4096
-// 7.6, 9.1; 6144x4096 10.4, 11.4; 9728x4096 13.5, 17.2; 4096x14336 21.5, 24.1; past the rule 8192x8192
-// 21.6, 20.3; 5120x13824 35.6, 29.7; 12288x4096 (a second round of tiles) 18.9, 17.0.
+// us, rows against tc (BF16, 32-bit scales, zero points, groups of 128): 256x8192 4.4, 8.9; 4096x4096
+// 7.5, 9.1; 6144x4096 10.8, 10.6; 9728x4096 13.6, 16.7; 4096x14336 21.4, 23.3; past the rule 8192x8192
+// 21.7, 19.5; 5120x13824 36.0, 24.0; 12288x4096 (a second round of tiles) 18.9, 18.2.
 bool small_for_rows(const W4Args& a, int sms) {
     return (a.N + kRwRows - 1) / kRwRows <= static_cast<uint64_t>(sms) * RwCfg<2>::kResident && static_cast<uint64_t>(a.N) * a.K < 1ull << 26;
 }
