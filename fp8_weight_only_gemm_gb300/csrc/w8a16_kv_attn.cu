@@ -9,7 +9,7 @@
 // m moves only when a y exceeds it by more than 8 (few steps do after the first; moving it
 // means rescaling O). The value scale is part of the maximum, so P_j <= 2^15 whatever the
 // scales are, and P is rounded once, to FP16: 11 bits, with 2^-31 of the largest weight
-// still representable. Both products run on FP16 operands: E4M3 converts to FP16 exactly
+// still representable (l adds the rounded P where they have these bits). Both products run on FP16 operands: E4M3 converts to FP16 exactly
 // (one instruction for two codes), and the query row is multiplied by a power of two
 // that puts its largest element in [2^7, 2^8), so BF16 queries are exact too down to
 // 2^-21 of their row's maximum. A non-finite query makes its row's outputs NaN.
@@ -55,6 +55,7 @@ constexpr uint32_t kMaxRows = 16;              // query rows of a tile: 8 NR
 constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (MMA M of the first product, K of the second)
 constexpr uint32_t kUnitKeys = kWarps * kStepKeys;
 constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
+constexpr float kNormalP = 6.103515625e-05f;   // 2^-14: above it FP16 keeps 11 bits
 
 // DP: the head size rounded up to 64, 128 or 256. NR: tiles of 8 query rows, 1 or 2.
 template <uint32_t DP, uint32_t NR>
@@ -421,10 +422,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
                     const float d = m[t][e] == -INFINITY ? 0.f : lv - m[t][e] + kPBits;
                     y[e] = ex2(fmaf(s[t][e], f[t][e], d));
                     y[2 + e] = ex2(fmaf(s[t][2 + e], f[t][e], d));
-                    l[t][e] = fmaf(y[e] + y[2 + e], iv, l[t][e]);
                 }
-                pb[t][0] = transpose8x8(pack2<true>(y[0], y[1]));
-                pb[t][1] = transpose8x8(pack2<true>(y[2], y[3]));
+                // The sum takes the weights as they were rounded: where one key has most of it, the rounding
+                // cancels. Small ones as they are: a page with a small scale has small P and large P / vs.
+                const uint32_t w0 = pack2<true>(y[0], y[1]), w1 = pack2<true>(y[2], y[3]);
+                const float2 r0 = unpack2<true>(w0), r1 = unpack2<true>(w1);
+                const auto kept = [](float x, float rounded) { return x > kNormalP ? rounded : x; };
+                l[t][0] = fmaf(kept(y[0], r0.x) + kept(y[2], r1.x), iv, l[t][0]);
+                l[t][1] = fmaf(kept(y[1], r0.y) + kept(y[3], r1.y), iv, l[t][1]);
+                pb[t][0] = transpose8x8(w0);
+                pb[t][1] = transpose8x8(w1);
             }
             // ---- outputs
             uint32_t vw[4][C::kVBytes / 4];   // keys 2 c, 2 c + 1, 8 + 2 c, 9 + 2 c
