@@ -92,27 +92,47 @@ __device__ __forceinline__ uint64_t seq_units(const AttnArgs& p, uint32_t b, boo
     return static_cast<uint64_t>(it.tiles) * it.units * p.c.kv_heads;
 }
 
-// Units of all sequences (every thread gets the sum).
-__device__ __forceinline__ uint64_t count_units(const AttnArgs& p, uint64_t* sh) {
-    uint64_t x = 0;
-    for (uint32_t i = threadIdx.x; i < p.b.batch; i += kThreads) x += seq_units(p, i, blockIdx.x == 0);
-    x = warp_sum(x);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+// Units of all sequences (every thread gets the sum). `mine`, `before`: of sequence threadIdx.x and
+// ahead of it, where there are no more sequences than threads.
+__device__ __forceinline__ uint64_t count_units(const AttnArgs& p, uint64_t* sh, uint64_t& mine, uint64_t& before) {
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    mine = 0;
+    for (uint32_t i = threadIdx.x; i < p.b.batch; i += kThreads) mine += seq_units(p, i, blockIdx.x == 0);
+    uint64_t inc = mine;   // inclusive scan of the warp, then of the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= static_cast<uint32_t>(o)) inc += t;
+    }
+    if (lane == 31) sh[warp] = inc;
     __syncthreads();
     uint64_t all = 0;
+    before = inc - mine;
 #pragma unroll
-    for (uint32_t w = 0; w < kWarps; ++w) all += sh[w];
-    __syncthreads();
+    for (uint32_t w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh[w];
+        all += sh[w];
+    }
     return all;
 }
 
-// The sequence that holds unit `at` (below the total), and its first unit.
-__device__ __forceinline__ void find_unit(const AttnArgs& p, uint64_t at, uint64_t* sh, uint32_t& b, uint64_t& base) {
+// The sequence that holds unit `at` (below the total), and its first unit: of the counts already there, or,
+// for more sequences than threads, in blocks of them.
+__device__ __forceinline__ void find_unit(const AttnArgs& p, uint64_t at, uint64_t* sh, uint64_t mine, uint64_t before, uint32_t& b,
+                                          uint64_t& base) {
     uint64_t run = 0;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (uint32_t i0 = 0; i0 < p.b.batch; i0 += kThreads) {
+    if (p.b.batch <= kThreads) {
+        if (at >= before && at < before + mine) {
+            sh[kWarps] = before;
+            sh[kWarps + 1] = threadIdx.x;
+        }
+        __syncthreads();
+    }
+    for (uint32_t i0 = 0; p.b.batch > kThreads && i0 < p.b.batch; i0 += kThreads) {
         const uint32_t i = i0 + threadIdx.x;
         const uint64_t v = i < p.b.batch ? seq_units(p, i, false) : 0;
+        __syncthreads();    // sh has been read
         uint64_t inc = v;   // inclusive scan of the warp, then of the block
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
     }
     grid_dependency_wait();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint64_t total = count_units(p, sh), ctas = active_ctas(total, p.ctas);
+    uint64_t mine, before;
+    const uint64_t total = count_units(p, sh, mine, before), ctas = active_ctas(total, p.ctas);
     zero_keyless(p);
     if (blockIdx.x >= ctas) {
         if (threadIdx.x == 0) write_boundary(p.ws, 0, 0, 0, Seq{}, 0, 0, total, ctas);
@@ -187,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
     const uint64_t u_end = first_unit(blockIdx.x + 1, total, ctas);
     uint32_t b;
     uint64_t base;
-    find_unit(p, u, sh, b, base);
+    find_unit(p, u, sh, mine, before, b, base);
 
     uint8_t* const ring = smem + warp * C::kStages * C::kStageBytes;
     float* const merge = reinterpret_cast<float*>(ring);
@@ -212,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
             n_b = static_cast<uint64_t>(it.tiles) * it.units * p.c.kv_heads;
         }
         const uint64_t in_seq = u - base;
-        const uint32_t item = static_cast<uint32_t>(in_seq / it.units);
-        const uint32_t unit0 = static_cast<uint32_t>(in_seq % it.units);
+        const uint32_t item = static_cast<uint32_t>(divide(in_seq, it.units));
+        const uint32_t unit0 = static_cast<uint32_t>(in_seq - static_cast<uint64_t>(item) * it.units);
         const uint32_t nunits = static_cast<uint32_t>(min(static_cast<uint64_t>(it.units - unit0), u_end - u));
         const uint32_t h = item / it.tiles, row0 = (item % it.tiles) * C::kRows;
         const uint32_t nrows = static_cast<uint32_t>(seq.count) * p.group;

@@ -27,15 +27,20 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
     return v;
 }
 
+// a / b: the 64-bit division takes some 400 cycles, few calls need it.
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // The CTAs that get work (no more than there are units, so that none between the
 // first and the last CTA of an item is empty), the first unit of CTA c's range, and the
 // CTA that holds unit u.
 __device__ __forceinline__ uint64_t active_ctas(uint64_t units, uint32_t ctas) {
     return units < ctas ? units : ctas;
 }
-__device__ __forceinline__ uint64_t first_unit(uint64_t c, uint64_t units, uint64_t ctas) { return c * units / ctas; }
+__device__ __forceinline__ uint64_t first_unit(uint64_t c, uint64_t units, uint64_t ctas) { return divide(c * units, ctas); }
 __device__ __forceinline__ uint32_t cta_of(uint64_t u, uint64_t units, uint64_t ctas) {
-    return static_cast<uint32_t>(((u + 1) * ctas - 1) / units);
+    return static_cast<uint32_t>(divide((u + 1) * ctas - 1, units));
 }
 
 // What CTA c's range begins in, written by it at the head of the workspace for the launch

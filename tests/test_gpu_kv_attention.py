@@ -314,3 +314,14 @@ def test_many_rows_repeatable_strides_and_graph(w8):
     assert np.array_equal(wide[:, :, :128].double().cpu().numpy(), got) and wide[:, :, 128:].abs().sum() == 0
     bad = w8.kv_attention(case.cache, case.q, case.dtable + 100000, case.dlens)
     assert bad.shape == case.q.shape and w8.device_status(clear=True)[0] == 2
+
+
+@pytest.mark.parametrize("count,Hq", [(1, 4), (10, 8)])
+def test_more_sequences_than_threads(w8, count, Hq):
+    # 300 sequences: both kernels count the work of a block of them at a time
+    g = torch.Generator().manual_seed(count)
+    lens = (torch.randint(0, 70, (300,), generator=g) + count - 1).tolist()
+    lens[7] = lens[299] = 0
+    case = Case(lens, [count if n else 0 for n in lens], Hq, 2, 64, 16, "bf16", seed=41)
+    finite_cache(case, 41)
+    check(case, w8)
