@@ -31,11 +31,11 @@
 // between CTAs goes through the workspace in FP32 and a second, dependent kernel joins
 // its parts in a fixed order: the result depends on nothing but the arguments.
 //
-// Bound by: long caches, by HBM. 32 sequences up to 8191 take 68 us for 342 MB (5.0 TB/s, 75 % of a
+// Bound by: long caches, by HBM. 32 sequences up to 8191 take 67 us for 342 MB (5.1 TB/s, 76 % of a
 // plain copy's rate), one of 131000 55 us for 268 MB (4.9 TB/s); the loop over units alone runs at a
-// copy's rate, the rest is the schedule (5 us to the first codes: lengths, page, codes are
+// copy's rate, the rest is the schedule (4 us to the first codes: lengths, page, codes are
 // loads that wait for one another), the spread of the CTAs' ends and the join. Short ones
-// (1000 tokens: 9.3 us) are that latency. Small heads with few rows a key (16 sequences of some 1000,
+// (1000 tokens: 9.0 us) are that latency. Small heads with few rows a key (16 sequences of some 1000,
 // five tokens, heads of 64: 22 us for 43 MB) are bound by instructions and by the fixed work of an
 // item, 2 to 3 us a CTA. Rows: one tile of 8 if they fit, as a second doubles the products.
 #include <cuda_runtime.h>
