@@ -23,7 +23,7 @@
 //     T = sum a, sum (c - z) a = S - z T. Columns that tokens leave unused take other chunks of K
 //     (the operand is zero outside a column's own), so 8 (4) chunks need one set of sums and one
 //     folding.
-//   3 to 8, and up to 16 of a small product (w4_rows_kernel). The columns are the tokens, so a warp
+//   3 to 8, and more of a small product (w4_rows_kernel). The columns are the tokens, so a warp
 //     would normalise a chunk of activations for 32 rows only: they stay as they are and codes
 //     become code - z, exactly (nibbles under the exponent of 128 in BF16, 1024 in FP16; 128 + z,
 //     1024 + z comes off).
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kSwThreads, 4) w4_stream_kernel(const W4Args p
     join_cluster<F16, kSwRows, kSwThreads, MP>(p, sums, rank, 0, p.M, n0);
 }
 
-// ------------------------------------------------------------ 3 to 16 tokens --
+// --------------------------------------------- 3 to 8 tokens, and small products --
 // As the kernel above, a ring of codes and a part of K for every warp; fragments of the
 // activations are loaded from global memory a stage ahead. 32 rows a warp and four stages of 4 KB on
 // 3 CTAs an SM; 64 rows and two stages of 8 KB read the activations half as often and took 0.97 (BF16)
@@ -481,14 +481,15 @@ __global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kern
     __shared__ uint64_t full[kRwWarps][kRwStages];
     __shared__ int abort_flag;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * kRwRows;
+    const uint32_t rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * kRwRows, m0 = blockIdx.y * kTok,
+                   tokens = min(kTok, p.M - m0);
     const uint32_t stages = (p.K + kStageK - 1) / kStageK, groups = p.K / G;
     const uint32_t s_begin = static_cast<uint32_t>(static_cast<uint64_t>(rank) * stages / p.split),
                    s_end = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / p.split);
     uint8_t* const boxes = smem + warp * kRwStages * kRwBox;
     const uint16_t* a_row[NT];
 #pragma unroll
-    for (uint32_t n = 0; n < NT; ++n) a_row[n] = p.A + static_cast<size_t>(min(8 * n + g, p.M - 1)) * p.lda + 8 * c;
+    for (uint32_t n = 0; n < NT; ++n) a_row[n] = p.A + static_cast<size_t>(min(m0 + 8 * n + g, p.M - 1)) * p.lda + 8 * c;
 
     if (lane == 0) {
         for (uint32_t i = 0; i < kRwStages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
@@ -613,15 +614,15 @@ __global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kern
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[(warp * kTok + 8 * n + 2 * c + (e & 1)) * kRwRedPitch + 16 * t + 8 * (e >> 1) + g] = acc[t][n][e];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < p.M * kRwRows; i += kRwThreads) {
+    for (uint32_t i = threadIdx.x; i < tokens * kRwRows; i += kRwThreads) {
         const uint32_t m = i / kRwRows, r = i % kRwRows;
         float v = 0.f;
 #pragma unroll
         for (uint32_t w = 0; w < kRwWarps; ++w) v += red[(w * kTok + m) * kRwRedPitch + r];
         if (p.split > 1) sums[m * kRwRedPitch + r] = v;
-        else if (n0 + r < p.N) p.C[static_cast<size_t>(m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
+        else if (n0 + r < p.N) p.C[static_cast<size_t>(m0 + m) * p.ldc + n0 + r] = static_cast<uint16_t>(pack2<F16>(v, 0.f));
     }
-    if (p.split > 1) join_cluster<F16, kRwRows, kRwThreads, kTok>(p, sums, rank, 0, p.M, n0);
+    if (p.split > 1) join_cluster<F16, kRwRows, kRwThreads, kTok>(p, sums, rank, m0, tokens, n0);
 }
 
 // --------------------------------------------------------------- more tokens --
@@ -938,11 +939,11 @@ cudaError_t launch_stream(W4Args a, int sms, cudaStream_t s, std::string* err) {
 }
 template <bool F16, uint32_t NT, uint32_t G>
 cudaError_t launch_rows(W4Args a, int sms, cudaStream_t s, std::string* err) {
-    const uint32_t tiles = (a.N + kRwRows - 1) / kRwRows;
-    a.split = choose_split(tiles, static_cast<uint64_t>(sms) * RwCfg<NT>::kResident, (a.K + kStageK - 1) / kStageK, kRwWarps);
+    const uint32_t tiles = (a.N + kRwRows - 1) / kRwRows, tok_tiles = (a.M + 8 * NT - 1) / (8 * NT);
+    a.split = choose_split(static_cast<uint64_t>(tiles) * tok_tiles, static_cast<uint64_t>(sms) * RwCfg<NT>::kResident, (a.K + kStageK - 1) / kStageK, kRwWarps);
     Maps m;
     if (!m.make(a, kRwRows, 128, 0, 0, err)) return cudaErrorInvalidValue;
-    return launch_clusters(w4_rows_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, 1, 1), kRwThreads, RwCfg<NT>::kSmem, s);
+    return launch_clusters(w4_rows_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kRwThreads, RwCfg<NT>::kSmem, s);
 }
 template <bool F16, uint32_t NT, uint32_t G>
 cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
@@ -953,19 +954,25 @@ cudaError_t launch_tc(W4Args a, int sms, cudaStream_t s, std::string* err) {
     if (!m.make(a, kTcRows4, kTcStageK / 2, C::kTok, 64, err)) return cudaErrorInvalidValue;
     return launch_clusters(w4_tc_kernel<F16, NT, G>, a, m.w, m.a, dim3(tiles * a.split, tok_tiles, 1), kTcThreads4, C::kSmem, s);
 }
-// 9 to 16 tokens in one call of w4_rows_kernel: where its tiles run at once and the product is small.
-// us, rows against tc (BF16, 32-bit scales, zero points, groups of 128): 256x8192 4.4, 8.9; 4096x4096
-// 7.5, 9.1; 6144x4096 10.8, 10.6; 9728x4096 13.6, 16.7; 4096x14336 21.4, 23.3; past the rule 8192x8192
-// 21.7, 19.5; 5120x13824 36.0, 24.0; 12288x4096 (a second round of tiles) 18.9, 18.2.
+// More than 8 tokens by w4_rows_kernel, in tiles of 16: one tile where the rows' tiles run at once and the
+// product is small, more where it is smaller still. us, rows against tc (BF16, 32-bit scales, zero
+// points, groups of 128):
+//   16 tokens: 256x8192 4.4, 8.9; 4096x4096 7.5, 9.1; 6144x4096 10.8, 10.6; 9728x4096 13.6, 16.7; 4096x14336 21.4,
+//     23.3; past the rule 8192x8192 21.7, 19.5; 5120x13824 36.0, 24.0; 12288x4096 (a second round of tiles) 18.9, 18.2
+//   32: 256x8192 5.1, 9.7; 1024x4096 5.2, 7.0; 4096x2048 6.7, 7.4; 2044x5632 9.2, 9.9 (groups of 32: 10.1, 12.8); past
+//     it 4096x4096 10.5, 10.1; 4096x8192 19.7, 16.3
+//   64: 1024x4096 7.3, 8.3; past it 4096x2048 12.0, 9.3
 bool small_for_rows(const W4Args& a, int sms) {
-    return (a.N + kRwRows - 1) / kRwRows <= static_cast<uint64_t>(sms) * RwCfg<2>::kResident && static_cast<uint64_t>(a.N) * a.K < 1ull << 26;
+    const uint64_t weights = static_cast<uint64_t>(a.N) * a.K, tok_tiles = (a.M + 15) / 16;
+    if (tok_tiles > 1) return tok_tiles <= 65535 && weights < (3ull << 23) && weights * tok_tiles < 3ull << 23;
+    return (a.N + kRwRows - 1) / kRwRows <= static_cast<uint64_t>(sms) * RwCfg<2>::kResident && weights < 1ull << 26;
 }
 template <bool F16, uint32_t G>
 cudaError_t launch_tokens(const W4Args& a, int sms, cudaStream_t s, std::string* err) {
     return a.M == 1    ? launch_stream<F16, 1, G>(a, sms, s, err)
            : a.M == 2  ? launch_stream<F16, 2, G>(a, sms, s, err)
            : a.M <= 8  ? launch_rows<F16, 1, G>(a, sms, s, err)
-           : a.M <= 16 && small_for_rows(a, sms) ? launch_rows<F16, 2, G>(a, sms, s, err)
+           : small_for_rows(a, sms) ? launch_rows<F16, 2, G>(a, sms, s, err)
            : a.M <= 16 ? launch_tc<F16, 16, G>(a, sms, s, err)
                        : launch_tc<F16, 32, G>(a, sms, s, err);
 }

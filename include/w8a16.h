@@ -461,8 +461,8 @@ enum {
  * Within a group the sums are FP32 sums of exact products (BF16 activations below
  * 2^-31 of the largest beside them in K lose bits), and the scale multiplies each group's
  * sum in FP32: no weight is rounded. A non-finite activation makes its row's outputs
- * non-finite. One launch: clusters of CTAs share 32 to 128 rows of W; above 32 tokens, tiles
- * of 32 (each reads W again). Deterministic. flags: W8A16_FLAG_PDL (no work queued earlier on the stream may
+ * non-finite, a non-finite scale its column's. One launch: clusters of CTAs share 32 to 128 rows
+ * of W; above 8 tokens, tiles of 16 or 32 (each reads W again). Deterministic. flags: W8A16_FLAG_PDL (no work queued earlier on the stream may
  * write W, scale or zeros); without it the call, queued as a programmatic dependent,
  * waits for the previous kernel before it touches memory. Errors as w8a16_gemm. */
 W8A16_API int w8a16_gemm_w4(const void *A, uint32_t a_row_stride, uint32_t act_dtype, const void *W,

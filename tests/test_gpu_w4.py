@@ -80,6 +80,13 @@ def test_more_rows_than_tiles_at_once(w8, M):
     check(w8, M, 9763, 320, 64, "f16", False, True, seed=M)
 
 
+@pytest.mark.parametrize("M", [17, 32, 33, 70])
+def test_larger_products(w8, M):
+    check(w8, M, 9763, 1600, 32, "bf16", True, False, seed=M, lda_pad=8, ldc_pad=5)
+    check(w8, M, 9763, 1664, 128, "f16", True, True, seed=M + 1)
+    check(w8, M, 9763, 1600, 64, "bf16", False, True, seed=M + 2)
+
+
 @pytest.mark.parametrize("N,K", [(64, 8192), (256, 28672), (28672, 256), (512, 4096)])
 def test_long_and_wide(w8, N, K):
     for M in (1, 12, 32):
