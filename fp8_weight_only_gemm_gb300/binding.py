@@ -169,6 +169,28 @@ def _stream_handle(stream) -> int | None:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(stream, shape, dtype, device, *, kept=True, make=None):
+    """A tensor that a call on `stream` makes for itself. torch's allocator gives a freed block away again
+    behind the work of the stream that it was taken under, and of no other: under the current stream, a
+    block whose last use there is still to come could be handed to kernels on `stream`, and a workspace
+    dropped on return to others while they run. kept: returned to the caller, whose current stream
+    may be where it is used when it is dropped."""
+    import torch
+    make = make or torch.empty
+    device = torch.device(device)
+    if stream is not None and device.type == "cuda":
+        current, handle = torch.cuda.current_stream(device), _stream_handle(stream)
+        if handle != int(current.cuda_stream):
+            if not hasattr(stream, "cuda_stream"):
+                stream = (torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
+            with torch.cuda.stream(stream):
+                t = make(shape, dtype=dtype, device=device)
+            if kept:
+                t.record_stream(current)
+            return t
+    return make(shape, dtype=dtype, device=device)
+
+
 # -------------------------------------------------------------- pure host --
 def check_args(M, N, K, a_row_stride, c_row_stride, A=0, W=0, scale=0, C=0) -> int:
     return load().w8a16_check_args(A or None, a_row_stride, W or None, scale or None, C or None,
@@ -271,7 +293,7 @@ def gemm(A, W, scale, C=None, *, stream=None, plan: Plan | None = None, flags: i
     import torch
     M, N, K = _shapes(A, W, scale, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _new(stream, (M, N), torch.bfloat16, A.device)
     if C.dtype != torch.bfloat16 or C.shape[0] != M or C.shape[1] < N:
         raise ValueError("C must be bfloat16 [M, >=N]")
     _on_one_gpu(A, W, scale, C)
@@ -309,7 +331,7 @@ def gemm_ws(A, W, scale, C=None, *, workspace=None, stream=None, plan: Plan | No
     import torch
     M, N, K = _shapes(A, W, scale, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _new(stream, (M, N), torch.bfloat16, A.device)
     if C.dtype != torch.bfloat16 or C.shape[0] != M or C.shape[1] < N:
         raise ValueError("C must be bfloat16 [M, >=N]")
     _on_one_gpu(A, W, scale, C)
@@ -321,7 +343,7 @@ def gemm_ws(A, W, scale, C=None, *, workspace=None, stream=None, plan: Plan | No
     if workspace is None:
         with torch.cuda.device(A.device):
             need = max(workspace_bytes_for(M, N, K), workspace_bytes(M, K))
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=A.device)
+        workspace = _new(stream, max(16, need), torch.uint8, A.device, kept=False)
     ws_ptr, ws_bytes = (None, 0) if workspace is False else (workspace.data_ptr(), workspace.numel())
     with torch.cuda.device(A.device):
         rc = lib.w8a16_gemm_ws(A.data_ptr(), A.stride(0), W.data_ptr(), scale.data_ptr(), C.data_ptr(),
@@ -337,7 +359,7 @@ def gemm_noalloc(A, W, scale, C=None, *, stream=None, flags: int = 0):
     import torch
     M, N, K = _shapes(A, W, scale, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _new(stream, (M, N), torch.bfloat16, A.device)
     if C.dtype != torch.bfloat16 or C.shape[0] != M or C.shape[1] < N:
         raise ValueError("C must be bfloat16 [M, >=N]")
     _on_one_gpu(A, W, scale, C)
@@ -376,7 +398,7 @@ def split_activations(A, workspace=None, *, stream=None):
         raise ValueError("A must be a bfloat16 [M, K] tensor with unit column stride")
     M, K = A.shape
     if workspace is None:
-        workspace = torch.empty(max(16, workspace_bytes(M, K)), dtype=torch.uint8, device=A.device)
+        workspace = _new(stream, max(16, workspace_bytes(M, K)), torch.uint8, A.device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _on_one_gpu(A, workspace)
@@ -396,7 +418,7 @@ def gemm_split_terms(workspace, M, W, scale, C=None, *, stream=None, flags: int 
     N, K = W.shape
     _scale_shape(scale, N, K)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=W.device)
+        C = _new(stream, (M, N), torch.bfloat16, W.device)
     if C.dtype != torch.bfloat16 or C.shape[0] != M or C.shape[1] < N or C.stride(1) != 1:
         raise ValueError("C must be bfloat16 [M, >=N] with unit column stride")
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -465,9 +487,8 @@ def quantize_weights(W, *, stream=None):
     if not W.is_cuda:
         raise ValueError("W must be on a CUDA device")
     N, K = W.shape
-    codes = torch.empty((N, K), dtype=torch.uint8, device=W.device)
-    scale = torch.empty(((N + 127) // 128, K // 128 if K % 128 == 0 else 1), dtype=torch.float32,
-                        device=W.device)
+    codes = _new(stream, (N, K), torch.uint8, W.device)
+    scale = _new(stream, ((N + 127) // 128, K // 128 if K % 128 == 0 else 1), torch.float32, W.device)
     with torch.cuda.device(W.device):
         rc = load().w8a16_quantize_weights(W.data_ptr(), wt, W.stride(0), N, K, codes.data_ptr(),
                                            scale.data_ptr(), _stream_handle(stream))
@@ -484,8 +505,8 @@ def quantize_activations(A, *, stream=None):
         raise ValueError("A must be a CUDA bfloat16 [M, K] tensor with contiguous rows")
     M, K = A.shape
     S = (M + 3) // 4 * 4
-    codes = torch.empty((M, K), dtype=torch.uint8, device=A.device)
-    scales = torch.zeros((max(K // 128, 1), S), dtype=torch.float32, device=A.device)
+    codes = _new(stream, (M, K), torch.uint8, A.device)
+    scales = _new(stream, (max(K // 128, 1), S), torch.float32, A.device, make=torch.zeros)
     with torch.cuda.device(A.device):
         rc = load().w8a16_quantize_activations(A.data_ptr(), A.stride(0), M, K, codes.data_ptr(),
                                                scales.data_ptr(), S, _stream_handle(stream))
@@ -513,7 +534,7 @@ def gemm_w8a8(A_codes, a_scale, W, scale, C=None, *, stream=None, plan: Plan | N
         raise ValueError("block_scale must be contiguous float32")
     _scale_shape(scale, N, K)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A_codes.device)
+        C = _new(stream, (M, N), torch.bfloat16, A_codes.device)
     if C.dtype != torch.bfloat16 or C.dim() != 2 or C.stride(1) != 1 or C.shape[0] != M or C.shape[1] < N:
         raise ValueError("C must be bfloat16 [M, >=N] with contiguous rows")
     _on_one_gpu(A_codes, a_scale, W, scale, C)
@@ -628,8 +649,7 @@ def kv_append(cache, k, v, page_table, lens, cos=None, sin=None, *, q=None, q_ou
         if q_out is not None:
             raise ValueError("q_out without q")
     elif q_out is None:
-        import torch
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new(stream, q.shape, q.dtype, q.device)
     rc = (_marshal or _load_marshal()).kv_append(
         cache._address, cache._index, cache.head_dim, k, v, page_table, lens, cu_q, max_q, q, q_out, cos, sin,
         interleaved, stream if stream is None else _stream_handle(stream))
@@ -657,15 +677,13 @@ def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu
     defaults to head_dim ** -0.5. workspace: a CUDA uint8 tensor of
     kv_attention_workspace_bytes(...) bytes that no concurrent call uses (None allocates
     one for this call). Returns out, [tokens, heads, head_dim] of q's dtype."""
-    if out is None or workspace is None:
+    if out is None:
+        out = _new(stream, q.shape, q.dtype, q.device)
+    if workspace is None:
         import torch
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if workspace is None:
-            B = page_table.shape[0]
-            most = max_q if max_q is not None else -(-q.shape[0] // max(B, 1))
-            workspace = torch.empty(kv_attention_workspace_bytes(cache, B, most, q.shape[1]), dtype=torch.uint8,
-                                    device=q.device)
+        B = page_table.shape[0]
+        most = max_q if max_q is not None else -(-q.shape[0] // max(B, 1))
+        workspace = _new(stream, kv_attention_workspace_bytes(cache, B, most, q.shape[1]), torch.uint8, q.device, kept=False)
     rc = (_marshal or _load_marshal()).kv_attention(
         cache._address, cache._index, cache.head_dim, q, out, page_table, lens, cu_q, max_q,
         cache.head_dim ** -0.5 if softmax_scale is None else softmax_scale, workspace,
@@ -683,8 +701,7 @@ def gemm_w4(A, W, scale, C=None, *, zeros=None, stream=None, flags: int = 0):
     dtype, [N, K/group] with group 32, 64 or 128 (taken from its shape); zeros: uint8
     [N, K/group], 0..15 (None: 8); C: optional [M, >=N] of A's dtype."""
     if C is None:
-        import torch
-        C = torch.empty((A.shape[0], W.shape[0]), dtype=A.dtype, device=A.device)
+        C = _new(stream, (A.shape[0], W.shape[0]), A.dtype, A.device)
     rc = (_marshal or _load_marshal()).gemm_w4(A, W, scale, C, zeros, flags,
                                                stream if stream is None else _stream_handle(stream))
     if rc:
