@@ -794,6 +794,7 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
             zp = z[0];
         };
         load_params(0);
+        if (p.early) grid_dependency_wait();   // the limit of the waits below starts behind the previous kernel: they are for its outputs
         float f[2] = {};   // scales of the products in flight
         const auto done = [&](uint32_t i, uint32_t slot) {   // the product of chunk i, in this slot
             const bool ok = wait_warp(smem_u32(&d_full[slot]), (i >> 1) & 1, p.timeout_ns, &abort_flag);
