@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         }
                         const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
                         // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
-                        rowf = bad ? rs.scale : fmaxf(rs.scale, kMinRowScale);
+                        // (a padding row, one that sees no key, is zero whatever its query holds)
+                        rowf = bad && row_end > 0 ? rs.scale : fmaxf(rs.scale, kMinRowScale);
 #pragma unroll
                         for (uint32_t un = 0; un < DP / 8; ++un) {
                             uint32_t o[4];
