@@ -327,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
             const bool bad = (__ballot_sync(0xFFFFFFFFu, !finite) >> (4 * g) & 15u) != 0u;   // by the row's four lanes
             const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
-            // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
-            // (a padding row is one that sees no key: it is zero whatever its query holds)
-            const float mine = bad && before + static_cast<int>(row / p.group) > 0 ? rs.scale : fmaxf(rs.scale, kMinRowScale);
+            // a padding row is one that sees no key: it is zero whatever its query holds
+            const float mine = bad && before + static_cast<int>(row / p.group) <= 0 ? 0.f : rs.scale;
 #pragma unroll
             for (uint32_t e = 0; e < 2; ++e) {
                 row_scale[t][e] = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * c + e));
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
                 for (int e = 0; e < 2; ++e) {
                     s[t][e] += s2[t][e];
                     s[t][2 + e] += s2[t][2 + e];
-                    f[t][e] = ks * row_scale[t][e];
+                    f[t][e] = logit_factor(ks, row_scale[t][e]);
                     if (edge) {
                         if (key + static_cast<int>(g) >= row_end[t][e]) s[t][e] = -INFINITY;
                         if (key + 8 + static_cast<int>(g) >= row_end[t][e]) s[t][2 + e] = -INFINITY;

@@ -136,8 +136,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The row scale of a query: softmax scale times 2^(E - 7) for its largest element's
 // exponent E, and the two factors f1 f2 = 2^(7 - E) that bring the row to [2^7, 2^8)
-// (two: E reaches -133 for BF16 subnormals). A row with a non-finite element gets a NaN scale.
-constexpr float kMinRowScale = 1.3552527156068805e-20f;   // 2^-66
+// (two: E reaches -133 for BF16 subnormals). What reaches the logits is its product with a page's
+// key scale (2^-60 and more), and only that has to be in FP32's range: a row scale below 2^-60 is
+// kept times -2^64, and its sign tells logit_factor. A row with a non-finite element gets a NaN scale.
 struct RowScale {
     float scale, f1, f2;
 };
@@ -146,7 +147,14 @@ __device__ __forceinline__ RowScale row_scale_of(float amax, bool bad, float sca
     const int E = amax > 0.f ? ilogbf(amax) : 7;
     const int a = (7 - E) / 2, b = 7 - E - a;
     const auto pow2 = [](int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); };
-    return {scale_log2 * pow2(-a) * pow2(-b), pow2(a), pow2(b)};
+    const float scale = scale_log2 * pow2(-a) * pow2(-b);
+    return {scale < kMinScale ? -(scale_log2 * pow2(64 - a) * pow2(-b)) : scale, pow2(a), pow2(b)};
+}
+// Logit per unit of score of a row and page. Never 0, so that a masked score (-inf) stays one (where
+// the smallest normal number shows in it, all logits are below 2^-75).
+__device__ __forceinline__ float logit_factor(float ks, float row_scale) {
+    constexpr float kTwoToMinus64 = 5.421010862427522e-20f, kSmallest = 1.1754943508222875e-38f;
+    return fmaf(row_scale < 0.f ? ks * kTwoToMinus64 : ks, fabsf(row_scale), kSmallest);
 }
 
 // The kernel for many query rows per key/value head (w8a16_kv_attn_tc.cu).

@@ -284,7 +284,7 @@ __device__ __forceinline__ void mask_scores(uint32_t (&v)[32], int first, int en
     for (int e = 0; e < 32; ++e)
         if (first + e >= end) v[e] = 0xFF800000u;
 }
-// Their largest y = score ks rowf + log2(vs) (ks rowf > 0: that of the largest score);
+// Their largest y = score f + log2(vs) (f = logit_factor > 0: that of the largest score);
 // ks, lv (and iv): of the two groups of 16 keys.
 __device__ __forceinline__ float score_max(const uint32_t (&v)[32], const float* ks, const float* lv, float rowf) {
     float y = -INFINITY;
@@ -293,7 +293,7 @@ __device__ __forceinline__ float score_max(const uint32_t (&v)[32], const float*
         float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) mx = max3(mx, __uint_as_float(v[16 * g + e]), __uint_as_float(v[16 * g + e + 1]));
-        y = fmaxf(y, fmaf(mx, ks[g] * rowf, lv[g]));
+        y = fmaxf(y, fmaf(mx, logit_factor(ks[g], rowf), lv[g]));
     }
     return y;
 }
@@ -303,7 +303,7 @@ __device__ __forceinline__ float score_weights(const uint32_t (&v)[32], const fl
     const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        const float f = ks[g] * rowf, d = lv[g] - rc;
+        const float f = logit_factor(ks[g], rowf), d = lv[g] - rc;
         const uint64_t ff = pack_f32x2(f, f), dd = pack_f32x2(d, d);
         uint64_t s2 = pack_f32x2(0.f, 0.f);
 #pragma unroll
@@ -435,9 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                             mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
                         }
                         const RowScale rs = row_scale_of(mx, bad, p.scale_log2);
-                        // kept above 0, so that a masked score (-inf) stays one: below 2^-66 all logits are 0 anyway
-                        // (a padding row, one that sees no key, is zero whatever its query holds)
-                        rowf = bad && row_end > 0 ? rs.scale : fmaxf(rs.scale, kMinRowScale);
+                        // a padding row is one that sees no key: it is zero whatever its query holds
+                        rowf = bad && row_end <= 0 ? 0.f : rs.scale;
 #pragma unroll
                         for (uint32_t un = 0; un < DP / 8; ++un) {
                             uint32_t o[4];
