@@ -123,6 +123,17 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
     return mbar_wait(bar, parity, globaltimer_ns() + timeout_ns, abort_flag, st, detail);
 }
 
+// After a wait that gave up: waits for the copies of steps first .. end - 1 into a ring of STAGES slots, step q
+// in slot q % STAGES, a barrier each. Until they have landed the ring may neither be reused nor left (its
+// shared memory is another CTA's then). The limit is its own: the abort flag is raised by now.
+template <uint32_t STAGES>
+__device__ __noinline__ void ring_drain(const uint64_t* full, uint32_t first, uint32_t end, uint64_t timeout_ns, DeviceStatus* st,
+                                        unsigned int detail) {
+    int none = 0;
+#pragma unroll 1
+    for (uint32_t q = first; q < end; ++q) mbar_wait_for(smem_u32(full + q % STAGES), (q / STAGES) & 1, timeout_ns, &none, st, detail);
+}
+
 // 16-byte asynchronous copy global -> shared through L2 only (the source may have
 // been written by the previous grid), and its group bookkeeping.
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {

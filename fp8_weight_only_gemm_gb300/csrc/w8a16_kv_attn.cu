@@ -54,6 +54,7 @@ constexpr uint32_t kWarps = 4, kThreads = 32 * kWarps;
 constexpr uint32_t kMaxRows = 16;              // query rows of a tile: 8 NR
 constexpr uint32_t kStepKeys = 16;             // keys of a warp's step (MMA M of the first product, K of the second)
 constexpr uint32_t kUnitKeys = kWarps * kStepKeys;
+constexpr uint32_t kStopped = 0x80000000u;
 constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
 constexpr float kNormalP = 6.103515625e-05f;   // 2^-14: above it FP16 keeps 11 bits
 
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
     for (uint32_t i = 0; i < C::kKChunks; ++i) k_at[i] = g * D + min(i * 64 + c * 16, D - 16);
 #pragma unroll
     for (uint32_t i = 0; i < C::kVPieces; ++i) v_at[i] = (kStepKeys + 2 * c) * D + min(g * C::kVPiece + i * 8 * C::kVPiece, D - C::kVPiece);
-    uint32_t taken = 0;   // steps of this warp so far
+    uint32_t taken = 0;   // steps of this warp so far; kStopped once a wait has given up
     bool first_part = true;
 
     while (u < u_end) {
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
 
         // ---- this warp's steps: 16 keys of each unit
         const int key0 = static_cast<int>(unit0 * kUnitKeys + warp * kStepKeys);
-        const uint32_t nsteps = static_cast<uint32_t>(max(0, min(static_cast<int>(nunits), (tile_end - key0 + static_cast<int>(kUnitKeys) - 1) / static_cast<int>(kUnitKeys))));
+        const uint32_t nsteps = taken == kStopped ? 0u : static_cast<uint32_t>(max(0, min(static_cast<int>(nunits), (tile_end - key0 + static_cast<int>(kUnitKeys) - 1) / static_cast<int>(kUnitKeys))));
         // Lane l holds what step l (mod 32) of a batch of 32 needs; a batch is asked for kStages - 1
         // steps before its first use, and its scales are first touched there.
         int meta_page = 0;
@@ -358,8 +359,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
         for (uint32_t step = 0; step < nsteps; ++step) {
             const uint32_t at = (taken + step) % C::kStages, parity = ((taken + step) / C::kStages) & 1;
             if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&full[warp][at]), parity) ||
-                                             wait_slow(smem_u32(&full[warp][at]), parity, p.timeout_ns, &abort_flag)))
+                                             wait_slow(smem_u32(&full[warp][at]), parity, p.timeout_ns, &abort_flag))) {
+                ring_drain<C::kStages>(full[warp], taken + step, taken + min(step + C::kStages - 1, nsteps), p.timeout_ns, &g_kv_attn_status, 2);
+                taken = kStopped - nsteps;   // the phases no longer count: no steps of later items
                 break;
+            }
             if ((step & 31u) == 0u) {   // the batch of 32 that the copies have reached
                 cur_k = meta_k < kMinScale ? kMinScale : meta_k;
                 const float v = meta_v < kMinScale ? kMinScale : meta_v;

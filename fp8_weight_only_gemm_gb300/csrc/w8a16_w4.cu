@@ -313,7 +313,10 @@ __global__ void __launch_bounds__(kSwThreads, 4) w4_stream_kernel(const W4Args p
 #pragma unroll 1
     for (uint32_t i = 0; i < mine; ++i) {
         const uint32_t at = i % kSwStages;
-        if (!wait_warp(smem_u32(&full[warp][at]), (i / kSwStages) & 1, p.timeout_ns, &abort_flag)) break;
+        if (!wait_warp(smem_u32(&full[warp][at]), (i / kSwStages) & 1, p.timeout_ns, &abort_flag)) {
+            ring_drain<kSwStages>(full[warp], i, min(i + kSwStages - 1, mine), p.timeout_ns, &g_w4_status, 3);
+            break;
+        }
         // the slot before this one has been read by all lanes: the next copies may overwrite it
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -551,7 +554,10 @@ __global__ void __launch_bounds__(kRwThreads, RwCfg<NT>::kResident) w4_rows_kern
         for (uint32_t q = 0; q < (kGroups + 3) / 4; ++q) cz[q] = zp[q];
         load_params(i + 1);
         load_acts(i + 1);
-        if (!wait_warp(smem_u32(&full[warp][at]), (i / kRwStages) & 1, p.timeout_ns, &abort_flag)) break;
+        if (!wait_warp(smem_u32(&full[warp][at]), (i / kRwStages) & 1, p.timeout_ns, &abort_flag)) {
+            ring_drain<kRwStages>(full[warp], i, min(i + kRwStages, mine), p.timeout_ns, &g_w4_status, 3);
+            break;
+        }
         const uint8_t* const w = boxes + at * kRwBox + g * 128 + 4 * c;
 #pragma unroll
         for (uint32_t q = 0; q < kGroups; ++q) {
@@ -771,13 +777,10 @@ __global__ void __launch_bounds__(kTcThreads4, kTcResident)
         }
         // Nothing of this CTA's is in flight when it leaves: products, and (after a wait that gave up) copies.
         if (elected) {
+            int none = 0;   // not the abort flag, which may be raised: these waits have their own limit
             tc_commit(smem_u32(&drain));
-            mbar_wait_for(smem_u32(&drain), 0, p.timeout_ns, &abort_flag, &g_w4_status, 2);
-            if (!ok) {
-                int none = 0;   // not the raised flag: these waits have their own limit
-                for (uint32_t q = s > 0 ? s - 1 : 0; q < issued; ++q)
-                    mbar_wait_for(smem_u32(&full[q % C::kStages]), (q / C::kStages) & 1, p.timeout_ns, &none, &g_w4_status, 3);
-            }
+            mbar_wait_for(smem_u32(&drain), 0, p.timeout_ns, &none, &g_w4_status, 2);
+            if (!ok) ring_drain<C::kStages>(full, s > 0 ? s - 1 : 0, issued, p.timeout_ns, &g_w4_status, 3);
         }
         __syncwarp();
     } else {
