@@ -85,10 +85,13 @@ int check_heads(const char* who, const char* name, const w8a16_heads_t* h, uint3
     return W8A16_OK;
 }
 
-// Query rows that share a key/value head, at most 2^31 - 1.
-uint32_t rows_per_head(uint32_t max_q, uint32_t heads, uint32_t kv_heads) {
+// Query rows that share a key/value head, which the kernels count in 31 bits; 0 with an error where there are more.
+uint32_t rows_per_head(const char* who, uint32_t max_q, uint32_t heads, uint32_t kv_heads) {
     const uint64_t r = static_cast<uint64_t>(max_q) * (heads / kv_heads);
-    return r > 0x7FFFFFFFu ? 0x7FFFFFFFu : static_cast<uint32_t>(r);
+    if (r <= 0x7FFFFFFFu) return static_cast<uint32_t>(r);
+    api_fail(W8A16_ERR_RANGE, std::string(who) + ": max_q=" + u(max_q) + " rows of " + u(heads / kv_heads) +
+                                  " query heads a key/value head must be below 2^31 in all");
+    return 0;
 }
 
 }  // namespace
@@ -146,9 +149,12 @@ uint64_t w8a16_kv_attention_workspace_bytes(const w8a16_kv_cache_t* cache, uint3
             rc = api_fail(W8A16_ERR_ARG, std::string(who) + ": batch, max_q and heads must be positive, heads=" + u(heads) +
                                              " a multiple of kv_heads=" + u(cache->kv_heads));
         int sms = 0;
-        if (!rc) rc = w8a16::api_device(&sms);
         if (rc) return rc;
-        bytes = w8a16::kv_attn_ws_bytes(cache->head_dim, rows_per_head(max_q, heads, cache->kv_heads), sms);
+        const uint32_t rows = rows_per_head(who, max_q, heads, cache->kv_heads);
+        if (rows == 0) return static_cast<int>(W8A16_ERR_RANGE);
+        rc = w8a16::api_device(&sms);
+        if (rc) return rc;
+        bytes = w8a16::kv_attn_ws_bytes(cache->head_dim, rows, sms);
         return api_ok();
     });
     return bytes;
@@ -170,10 +176,12 @@ int w8a16_kv_attention(const w8a16_kv_cache_t* cache, const w8a16_kv_batch_t* ba
                                                u(cache->kv_heads) + " key/value heads");
         if (!(softmax_scale > 0.f) || softmax_scale > 1e30f)
             return api_fail(W8A16_ERR_ARG, std::string(who) + ": softmax_scale must be positive and finite");
+        const uint32_t rows = rows_per_head(who, batch->max_q, q->heads, cache->kv_heads);
+        if (rows == 0) return static_cast<int>(W8A16_ERR_RANGE);
         int sms = 0;
         rc = w8a16::api_device(&sms);
         if (rc) return rc;
-        const uint64_t need = w8a16::kv_attn_ws_bytes(cache->head_dim, rows_per_head(batch->max_q, q->heads, cache->kv_heads), sms);
+        const uint64_t need = w8a16::kv_attn_ws_bytes(cache->head_dim, rows, sms);
         if (!workspace || workspace_bytes < need)
             return api_fail(W8A16_ERR_ARG, std::string(who) + ": needs a workspace of " + u(need) + " bytes, got " +
                                                u(workspace ? workspace_bytes : 0));

@@ -738,8 +738,7 @@ int launch_kv_attn(const w8a16_kv_cache_t& c, const w8a16_kv_batch_t& b, uint32_
     AttnArgs p{c, b, q, out, static_cast<float*>(ws), softmax_scale * 1.4426950408889634f, q.heads / c.kv_heads, 0, 0, 0, timeout_ns};
     while ((1u << p.page_shift) < c.page_size) ++p.page_shift;
     const bool f16 = act_dtype == W8A16_ACT_F16;
-    const uint64_t rows = static_cast<uint64_t>(b.max_q) * p.group;
-    const cudaError_t e = kv_attn_tc_applies(c.head_dim, static_cast<uint32_t>(rows < 0x7FFFFFFFu ? rows : 0x7FFFFFFFu))
+    const cudaError_t e = kv_attn_tc_applies(c.head_dim, b.max_q * p.group)
                               ? launch_kv_attn_tc(p, f16, sms, s)
                               : f16 ? launch_dim<true>(p, sms, s) : launch_dim<false>(p, sms, s);
     if (e != cudaSuccess) {

@@ -415,7 +415,8 @@ W8A16_API int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_batc
  * over the positions j <= the query's own (causal from the end of the sequence; the
  * cache already holds the call's tokens: w8a16_kv_append first).
  *   q, out  [tokens][heads][head_dim], heads a multiple of kv_heads, BF16 or FP16
- *           (act_dtype), same shape; out must not overlap q
+ *           (act_dtype), same shape; out must not overlap q; max_q * heads / kv_heads
+ *           below 2^31 (W8A16_ERR_RANGE)
  * Scales may be any positive FP32 values (those below 2^-60 count as 2^-60). Both
  * products take FP16 operands with FP32 sums: the E4M3 codes are exact, a query is
  * exact down to 2^-21 of its head's largest element, and the softmax weights are
