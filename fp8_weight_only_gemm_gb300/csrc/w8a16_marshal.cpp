@@ -115,15 +115,19 @@ bool stream_of(PyObject* o, long index, w8a16_stream_t* out) {
     return !PyErr_Occurred();
 }
 
-// Runs `f` on device `index` without the interpreter lock; C++ errors become Python's.
+// Runs `f` on device `index` without the interpreter lock; C++ errors become Python's. The lock is back
+// before an exception is, whoever throws it.
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 PyObject* run(long index, F&& f) {
     int rc = 0;
     try {
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-        Py_BEGIN_ALLOW_THREADS
+        Unlocked unlocked;
         rc = f();
-        Py_END_ALLOW_THREADS
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -248,11 +252,13 @@ PyObject* gemm_w4_impl(PyObject* const* a) {
     const unsigned long flags = PyLong_AsUnsignedLong(a[5]);
     w8a16_stream_t stream;
     if (PyErr_Occurred() || !stream_of(a[6], index, &stream)) return nullptr;
+    const void *const Ap = A->data_ptr(), *const Wp = W->data_ptr(), *const Sp = S->data_ptr(), *const Zp = Z ? Z->data_ptr() : nullptr;
+    void* const Cp = C->data_ptr();
     return run(index, [&] {
-        return g_w4(A->data_ptr(), static_cast<uint32_t>(A->stride(0)), static_cast<uint32_t>(act), W->data_ptr(), S->data_ptr(),
-                    S->scalar_type() == at::kFloat ? W8A16_W4_SCALE_F32 : W8A16_W4_SCALE_ACT, Z ? Z->data_ptr() : nullptr,
-                    static_cast<uint32_t>(K / S->size(1)), C->data_ptr(), static_cast<uint32_t>(C->stride(0)), static_cast<uint32_t>(M),
-                    static_cast<uint32_t>(N), static_cast<uint32_t>(K), static_cast<uint32_t>(flags), stream);
+        return g_w4(Ap, static_cast<uint32_t>(A->stride(0)), static_cast<uint32_t>(act), Wp, Sp,
+                    S->scalar_type() == at::kFloat ? W8A16_W4_SCALE_F32 : W8A16_W4_SCALE_ACT, Zp, static_cast<uint32_t>(K / S->size(1)), Cp,
+                    static_cast<uint32_t>(C->stride(0)), static_cast<uint32_t>(M), static_cast<uint32_t>(N), static_cast<uint32_t>(K),
+                    static_cast<uint32_t>(flags), stream);
     });
 }
 
