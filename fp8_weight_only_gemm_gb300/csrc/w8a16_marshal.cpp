@@ -157,6 +157,12 @@ PyObject* kv_append_impl(PyObject* const* a) {
     const auto* cache = static_cast<const w8a16_kv_cache_t*>(PyLong_AsVoidPtr(a[0]));
     const long index = PyLong_AsLong(a[1]), dim = PyLong_AsLong(a[2]);
     if (PyErr_Occurred()) return nullptr;
+    if ((a[11] == Py_None) != (a[12] == Py_None)) {
+        PyErr_SetString(PyExc_ValueError, "cos and sin go together: one of them is None");
+        return nullptr;
+    }
+    const int interleaved = PyObject_IsTrue(a[13]);
+    if (interleaved < 0) return nullptr;
     const at::Tensor* k = tensor(a[3], "k");
     if (!k) return nullptr;
     const int act = act_type(*k, "k");
@@ -172,16 +178,16 @@ PyObject* kv_append_impl(PyObject* const* a) {
     if (with_q && (!heads(a[9], "q", rows, dim, type, index, &qd) || !heads(a[10], "q_out", rows, dim, type, index, &od))) return nullptr;
     w8a16_rope_t rope{nullptr, nullptr, 0, 0, 0};
     if (a[11] != Py_None) {
-        const at::Tensor *c = tensor(a[11], "cos"), *s = c && a[12] != Py_None ? tensor(a[12], "sin") : nullptr;
-        if (!c || (a[12] != Py_None && !s)) return nullptr;
-        if (!s || c->dim() != 2 || s->sizes() != c->sizes() || c->scalar_type() != at::kFloat || s->scalar_type() != at::kFloat ||
+        const at::Tensor *c = tensor(a[11], "cos"), *s = c ? tensor(a[12], "sin") : nullptr;
+        if (!s) return nullptr;
+        if (c->dim() != 2 || s->sizes() != c->sizes() || c->scalar_type() != at::kFloat || s->scalar_type() != at::kFloat ||
             !c->is_contiguous() || !s->is_contiguous()) {
             PyErr_SetString(PyExc_ValueError, "cos and sin must be contiguous float32 [positions, rotary_dim / 2]");
             return nullptr;
         }
         if (!on(*c, index, "cos") || !on(*s, index, "sin")) return nullptr;
         rope = {c->const_data_ptr<float>(), s->const_data_ptr<float>(), static_cast<uint32_t>(c->size(0)), static_cast<uint32_t>(2 * c->size(1)),
-                PyObject_IsTrue(a[13]) ? 1u : 0u};
+                interleaved ? 1u : 0u};
     }
     w8a16_stream_t stream;
     if (!stream_of(a[14], index, &stream)) return nullptr;
