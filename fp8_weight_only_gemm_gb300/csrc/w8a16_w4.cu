@@ -3,10 +3,10 @@
 // Mathematics.  C[m][n] = sum_g s[n][g] * ( sum_{k in g} A[m][k] (code[n][k] - z[n][g]) ).
 // Codes become operands of the tensor cores exactly, products add in FP32, a group's sum is
 // scaled once, in FP32: no weight is rounded. Bytes are HBM's to bound (0.5 a weight and the
-// scales); the integer pipe, at one instruction in two cycles, bounds the decoding, so the two
+// scales); the integer pipe, at one instruction in two cycles, bounds the decoding, so the three
 // kernels below spend as few integer operations on a word of eight codes as they can.
 //
-// Layout. m16n8k16 with 16 weight rows as M and 8 columns as N. A lane's 32-bit word holds 8
+// Layout (of the two kernels on mma.sync). m16n8k16 with 16 weight rows as M and 8 columns as N. A lane's 32-bit word holds 8
 // codes of a row, and masks take the pairs (k, k + 4) out of it; the order of a
 // contraction's index being free, the activations are paired the same way, and weights never
 // move between lanes.
@@ -18,8 +18,9 @@
 //   1 or 2 tokens (w4_stream_kernel). Every warp has a ring and a part of K of its own. The bits of
 //     a nibble, as FP16, are the subnormal number c 2^-24 (or 16 c 2^-24 four bits higher): four
 //     masks and a shift decode a word. The activations become FP16, times a power of two that
-//     puts the largest of a chunk of 32 at 2^14 (exact down to 2^-24 of it), and a sixteenth of
-//     that where the codes come times 16. The zero point leaves the product: with S = sum c a,
+//     puts the largest of a chunk of 32 at 2^14, and a sixteenth of that where the codes come times 16, the
+//     odd elements (exact down to 2^-27 of the largest for BF16, whose 8 bits end at FP16's 2^-24, and 2^-24 for
+//     FP16; 2^-31 and 2^-28 for even ones). The zero point leaves the product: with S = sum c a,
 //     T = sum a, sum (c - z) a = S - z T. Columns that tokens leave unused take other chunks of K
 //     (the operand is zero outside a column's own), so 8 (4) chunks need one set of sums and one
 //     folding.

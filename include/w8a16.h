@@ -355,7 +355,8 @@ typedef struct {
  * b's tokens of this call (cu_q NULL: max_q rows each, tokens = batch * max_q).
  * lens[b] is the sequence's length with these tokens, which are its last ones: token
  * t of T has position lens[b] - T + t. Tokens at negative positions (lens[b] < T)
- * are padding: not written, and without attention. Position p lives in slot
+ * are padding: not written, and without attention. Rows of no sequence (below cu_q[0],
+ * from cu_q[batch] on) are neither read into a result nor written. Position p lives in slot
  * p % page_size of page page_table[b*page_table_stride + p/page_size]. Device
  * memory but for the counts; max_q: the most rows of one sequence. */
 typedef struct {
@@ -421,7 +422,7 @@ W8A16_API int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_batc
  * products take FP16 operands with FP32 sums: the E4M3 codes are exact, a query is
  * exact down to 2^-21 of its head's largest element, and the softmax weights are
  * rounded once to 11 bits. Queries without a visible key (lens[b] = 0, padding) give
- * zeros; a query with a non-finite element gives NaN; what lies in slots past a
+ * zeros, whatever they hold; other queries with a non-finite element give NaN; what lies in slots past a
  * query's position has no effect, whatever its bits.
  *   workspace  device memory, 16-byte aligned, at least
  *              w8a16_kv_attention_workspace_bytes(cache, batch->batch, batch->max_q,
@@ -459,9 +460,11 @@ enum {
  *   zeros  [N][K/group] bytes in 0..15, 4-byte aligned, or NULL: 8 everywhere
  *   group  32, 64 or 128; K a positive multiple of it
  *   C      the activations' type [M][c_row_stride]; only columns < N are written
- * Within a group the sums are FP32 sums of exact products (BF16 activations below
- * 2^-31 of the largest beside them in K lose bits), and the scale multiplies each group's
- * sum in FP32: no weight is rounded. A non-finite activation makes its row's outputs
+ * Within a group the sums are FP32 sums of exact products, and the scale multiplies each group's
+ * sum in FP32: no weight is rounded. With one or two tokens, activations far below the largest
+ * of their 32 in K (from a multiple of 32 on) lose bits: below 2^-31 of it (BF16) or 2^-28 (FP16) at
+ * even positions, 2^-27 or 2^-24 at odd ones. A group's sum is formed before its scale: one beyond
+ * FP32's range (BF16 activations of some 1e35) overflows although the scaled sum would not. A non-finite activation makes its row's outputs
  * non-finite, a non-finite scale its column's. One launch: clusters of CTAs share 32 to 128 rows
  * of W; above 8 tokens, tiles of 16 or 32 (each reads W again). Deterministic. flags: W8A16_FLAG_PDL (no work queued earlier on the stream may
  * write W, scale or zeros); without it the call, queued as a programmatic dependent,
