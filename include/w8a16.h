@@ -563,8 +563,8 @@ typedef struct {
  * All in FP32 (layer norm: the mean first, then squares about it); h and y are rounded once each, and y is
  * of h before its rounding. Squares are FP32: rows with values beyond some 1e18 overflow. A
  * non-finite value makes NaN of its own row's y, where it stands at least. Quantised: codes [M][out_stride] and out_scale
- * as w8a16_gemm_w8a8 reads them (scale = amax / 448 of a row's 128, code = RNE of the
- * quotient; amax = 0: scale and codes 0; NaN: the NaN code, not in amax; out_scale_stride >= M
+ * as w8a16_gemm_w8a8 reads them (scale = amax / 448 of a row's 128, rounded to FP32, code = RNE of the
+ * FP32 quotient by it; scale 0: codes 0; NaN: the NaN code, not in amax; out_scale_stride >= M
  * and a multiple of 4, out_stride a multiple of 16). One launch, queued as a programmatic dependent that waits for the
  * previous kernel before it touches memory; with W8A16_FLAG_PDL the weights and biases are asked
  * for before that (no work queued earlier on the stream may write them). Deterministic. The order of a row's sums
