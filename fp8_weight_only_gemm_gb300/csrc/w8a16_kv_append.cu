@@ -226,6 +226,10 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& p, uint32_t n, 
     const int pos = seq.len - seq.count + t;
     Rows<AXES> rows{};
     const bool good = pos < 0 || rows_of<AXES>(p, n, pos, rows);
+    if (AXES ? !good : p.rope.rotary_dim != 0 && pos >= static_cast<int>(p.rope.rows)) {   // the block's one token: skipped whole
+        if (threadIdx.x == 0) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pos));
+        return;
+    }
     if constexpr (AXES) {
         if (pos >= 0) gather(p, n, g);
         __syncthreads();
@@ -234,10 +238,6 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& p, uint32_t n, 
     for (uint32_t u = 0; u < kQueryTasks; ++u) {
         if (first + u * kThreads >= tasks) break;
         if (pos < 0) ch[u].rotated = false;   // padding: passed through
-        if (ch[u].rotated && (AXES ? !good : pos >= static_cast<int>(p.rope.rows))) {
-            record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pos));
-            continue;
-        }
         float x[16];
         rotated<F16, AXES>(p, qa[u], qb[u], ch[u], i[u], rows, x, AXES ? g.cos : nullptr);
         uint32_t w[8];
