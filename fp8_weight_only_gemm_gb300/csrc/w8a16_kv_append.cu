@@ -107,9 +107,9 @@ template <bool AXES>
 struct Rows {
     int pos[AXES ? 4 : 1];
 };
-// Of row n of the call, at `pos` in its sequence. false: outside the table (they are 0 then, and may be used).
+// Of row n of the call, at `pos` in its sequence. false: outside the table (they are 0 then, and may be used); `bad` is one that is.
 template <bool AXES>
-__device__ __forceinline__ bool rows_of(const AppendArgs& p, uint32_t n, int pos, Rows<AXES>& r) {
+__device__ __forceinline__ bool rows_of(const AppendArgs& p, uint32_t n, int pos, Rows<AXES>& r, int& bad) {
     if constexpr (!AXES) {
         r.pos[0] = pos;
         return true;   // the callers look at the last position
@@ -118,7 +118,7 @@ __device__ __forceinline__ bool rows_of(const AppendArgs& p, uint32_t n, int pos
 #pragma unroll
         for (uint32_t a = 0; a < 4; ++a) {
             r.pos[a] = a < p.axes.axes ? p.axes.positions[a * p.axes.stride + n] : 0;
-            if (static_cast<uint32_t>(r.pos[a]) >= p.rope.rows) good = false, r.pos[a] = 0;
+            if (static_cast<uint32_t>(r.pos[a]) >= p.rope.rows) good = false, bad = r.pos[a], r.pos[a] = 0;
         }
         return good;
     }
@@ -225,9 +225,10 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& p, uint32_t n, 
     if (t < 0 || t >= seq.count) return;   // rows that no sequence claims (a bad one: reported by its items)
     const int pos = seq.len - seq.count + t;
     Rows<AXES> rows{};
-    const bool good = pos < 0 || rows_of<AXES>(p, n, pos, rows);
+    int bad = pos;
+    const bool good = pos < 0 || rows_of<AXES>(p, n, pos, rows, bad);
     if (AXES ? !good : p.rope.rotary_dim != 0 && pos >= static_cast<int>(p.rope.rows)) {   // the block's one token: skipped whole
-        if (threadIdx.x == 0) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(pos));
+        if (threadIdx.x == 0) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(bad));
         return;
     }
     if constexpr (AXES) {
@@ -304,10 +305,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
     const uint32_t tasks = static_cast<uint32_t>(hi - lo) * per_token;
 
     bool good = true;   // of the tokens that this lane has looked at: their rows of the table are there
+    int bad = 0;
     if constexpr (AXES)
         for (int t = lo + static_cast<int>(lane); t < hi; t += static_cast<int>(TPI)) {
             Rows<AXES> rows;
-            good = rows_of<AXES>(p, static_cast<uint32_t>(seq.first + t - first), t, rows) && good;
+            good = rows_of<AXES>(p, static_cast<uint32_t>(seq.first + t - first), t, rows, bad) && good;
         }
     // What each of the new tokens' tasks does, with its rotated values.
     const auto each = [&](auto&& use) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
                 const int pos = lo + static_cast<int>(task / per_token), n = seq.first + pos - first;
                 const Chunks ch = chunks_of(rot, p.rope.interleaved, i);
                 Rows<AXES> rows{};
-                if (!AXES || !is_v) rows_of<AXES>(p, static_cast<uint32_t>(n), pos, rows);
+                if (!AXES || !is_v) rows_of<AXES>(p, static_cast<uint32_t>(n), pos, rows, bad);
                 float x[16];
                 load_rotated<F16, AXES>(p, x0 + static_cast<int64_t>(n) * src.token_stride, ch, i, rows, x);
                 use(pos, ch, x);
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs p)
         for (uint32_t w = 0; w < kThreads / 32; ++w) bits = max(bits, warp_max[w]);
     }
     if (AXES && bits == 0xFFFFFFFFu) {
-        if (lane == 0) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(hi - 1));
+        if (!good) record_failure(&g_kv_append_status, W8A16_STATUS_BAD_INDEX, static_cast<uint32_t>(bad));
         return;
     }
     const float scale = fmaxf(page_scale(__uint_as_float(bits)), old);

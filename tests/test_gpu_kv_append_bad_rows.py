@@ -1,4 +1,5 @@
-"""A token whose row of the rotary table does not exist: its query is left as it was, the dims that are not rotated too."""
+"""A token whose row of the rotary table does not exist: its query is left as it was, the dims that are not rotated too,
+and the status holds the value that was out of range."""
 from __future__ import annotations
 
 import pytest
@@ -31,7 +32,8 @@ def test_an_axis_outside_the_table(w8, count, bad, interleaved):
     out = torch.full_like(case.q, 7.0)
     w8.kv_append(case.cache, case.k, case.v, case.dtable, case.dlens, cos, sin, q=case.q, q_out=out, interleaved=interleaved,
                  positions=pos.cuda(), axes=w8.RopeAxes.sections((8, 4, 4)))
-    assert w8.device_status(clear=True)[0] == 2
+    code, _, detail = w8.device_status(clear=True)
+    assert (code, detail) == (2, bad % (1 << 32))
     assert (out[count - 1] == 7).all()
     rest = torch.arange(2 * count, device="cuda") != count - 1
     assert torch.equal(out[rest][..., 32:], case.q[rest][..., 32:])
