@@ -379,7 +379,8 @@ PyObject* norm_residual_impl(PyObject* const* a) {
             return refuse(PyExc_TypeError, "weights and biases must have one type, float32 or x's");
         first = t;
     }
-    if (g && (g->dim() != 2 || g->size(1) != H || g->stride(1) != 1 || g->size(0) > 0xFFFFFFFFll || g->scalar_type() != x->scalar_type()))
+    // (without rows its pointer would be NULL, which is a call without a gate)
+    if (g && (g->dim() != 2 || g->size(0) < 1 || g->size(1) != H || g->stride(1) != 1 || g->size(0) > 0xFFFFFFFFll || g->scalar_type() != x->scalar_type()))
         return refuse(PyExc_ValueError, "gate must be [rows, H] of x's type with contiguous rows");
     const double scale = PyFloat_AsDouble(a[10]), eps = PyFloat_AsDouble(a[11]);
     const unsigned long kind = PyLong_AsUnsignedLong(a[12]), flags = PyLong_AsUnsignedLong(a[13]);
