@@ -62,6 +62,9 @@ constexpr uint32_t kStages = 2;
 constexpr uint32_t kRing = 8, kLook = 4;        // units whose pages and scales are held, and looked up at a time
 constexpr float kPBits = 7.f, kRise = 8.f;     // P = 2^(y - m + 7); m moves when exceeded by 8
 constexpr uint32_t kChunk = 256;               // sequences whose unit counts are held at a time
+constexpr uint32_t kNanWords = 64;             // of the map of those groups of 16 keys in whose values clean_tile found a NaN
+// The bit there of group i of a CTA with `units` units, eight groups each: one a group, where there are bits enough.
+__device__ __forceinline__ uint32_t nan_bit(uint32_t i, uint32_t units) { return i / (8 * units / (32 * kNanWords) + 1); }
 
 constexpr uint32_t kTurnBytes = 32 * 64;        // 64 bytes of a warp's 32 rows
 
@@ -86,6 +89,7 @@ struct Tail {
     uint32_t tmem;
     int abort_flag;
     int nan_seen;
+    uint32_t nan_groups[kNanWords];
     Look look[kRing];
 };
 static_assert(sizeof(Tail) <= 2048, "barrier block");
@@ -306,13 +310,20 @@ __device__ __forceinline__ void convert16(const uint4& q, uint4& lo, uint4& hi) 
 }
 // NaN values (FP16) that this lane has stored to a V tile: 0 for the products, marked in the
 // outputs at the end (mark_nan). For units where some rows do not see all keys: there 0 * NaN
-// would reach them.
-__device__ __noinline__ void clean_tile(uint8_t* even, uint8_t* odd, uint32_t chunks, uint32_t halves, uint32_t half_bytes, Tail* tl) {
+// would reach them. But for kFull, whose marking reads all such keys again, the groups that held one are noted: `group` is
+// that of the warp's first keys, of a CTA with `units` units.
+template <bool NOTED>
+__device__ __noinline__ void clean_tile(uint8_t* even, uint8_t* odd, uint32_t chunks, uint32_t halves, uint32_t half_bytes, Tail* tl, uint32_t group = 0,
+                                        uint32_t units = 0) {
     for (uint32_t i = 0; i < 2 * chunks; ++i) {
         uint16_t* at = reinterpret_cast<uint16_t*>((i & 1 ? odd : even) + i / 2 % halves * half_bytes + i / 2 / halves * 1024);
         for (int e = 0; e < 8; ++e)
             if ((at[e] & 0x7FFF) > 0x7C00) {
                 at[e] = 0;
+                if constexpr (NOTED) {
+                    const uint32_t bit = nan_bit(group + i / 2 / halves / 2, units);   // (8 keys a step)
+                    atomicOr(&tl->nan_groups[bit / 32], 1u << bit % 32);
+                }
                 *static_cast<volatile int*>(&tl->nan_seen) = 1;
             }
     }
@@ -395,24 +406,46 @@ __device__ __noinline__ void mark_nan(const AttnArgs& p, uint32_t b, uint32_t h,
     }
 }
 
-// But for kFull: the same of the keys of groups [v_lo, v_hi) that a row sees whose keys end at row_end; marks lie `stride` floats apart.
+// But for kFull: the same of the keys of an item's units [j0, j0 + cnt) that a row sees whose keys end at row_end; marks lie `stride`
+// floats apart. Only the groups that clean_tile found a NaN in are read again, 16 codes a load (the other warps wait meanwhile, and a
+// prefix that some rows end in goes through clean_tile whole): `unit0` is the CTA's number of the first unit, of `units`.
 template <SpanMode MODE>
-__device__ __noinline__ void mark_nan_span(const AttnArgs& p, uint32_t b, uint32_t h, const Groups& span, int v_lo, int v_hi, int row_end, uint16_t* dst,
-                                           float* part, uint32_t stride) {
+__device__ __noinline__ void mark_nan_span(const AttnArgs& p, const Tail* tl, uint32_t unit0, uint32_t units, uint32_t b, uint32_t h, const Groups& span,
+                                           uint32_t j0, uint32_t cnt, int row_end, uint16_t* dst, float* part, uint32_t stride) {
     const int lo = row_lo<MODE>(p, row_end);
-    for (int i = 16 * v_lo; i < 16 * min(v_hi, span.count); ++i) {
-        const int key = group_key(span, i / 16) + i % 16;
-        if (key >= row_end || (key < lo && key >= sinks_of<MODE>(p))) continue;
-        const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (key >> p.page_shift)];
+    const auto found = [&](uint32_t bit) { return (static_cast<const volatile uint32_t*>(tl->nan_groups)[bit / 32] >> bit % 32 & 1u) != 0; };
+    uint64_t marked[2] = {0, 0};   // dims, 64 each
+    const uint32_t pieces = p.c.head_dim / 16;
+    for (uint32_t v = 8 * j0; v < min(8 * (j0 + cnt), static_cast<uint32_t>(span.count)); ++v) {
+        if (!found(nan_bit(8 * (unit0 - j0) + v, units))) continue;
+        const int first = group_key(span, static_cast<int>(v));
+        const int page = p.b.page_table[static_cast<int64_t>(b) * p.b.page_table_stride + (first >> p.page_shift)];
         if (page < 0 || page >= static_cast<int>(p.c.num_pages)) continue;
-        const uint8_t* v = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(page) * p.c.page_stride +
-                           static_cast<int64_t>(h) * p.c.head_stride +
-                           static_cast<int64_t>(key & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
-        for (uint32_t d = 0; d < p.c.head_dim; ++d)
-            if ((v[d] & 0x7F) == 0x7F) {
-                if (dst) dst[d] = 0x7FC0u;
-                else part[d * stride] = __uint_as_float(0x7FC00000u);
+        const uint8_t* codes = static_cast<const uint8_t*>(p.c.v_codes) + static_cast<int64_t>(page) * p.c.page_stride +
+                               static_cast<int64_t>(h) * p.c.head_stride +
+                               static_cast<int64_t>(first & static_cast<int>(p.c.page_size - 1)) * p.c.token_stride;
+#pragma unroll 1
+        for (int key = first; key < first + 16; ++key, codes += p.c.token_stride) {
+            if (key >= row_end || (key < lo && key >= sinks_of<MODE>(p))) continue;
+#pragma unroll
+            for (uint32_t half = 0; half < 2; ++half) {
+                uint32_t any = 0;
+#pragma unroll
+                for (uint32_t c = 4 * half; c < 4 * half + 4; ++c) {
+                    const uint4 q = c < pieces ? __ldg(reinterpret_cast<const uint4*>(codes) + c) : make_uint4(0, 0, 0, 0);
+                    any |= e4m3_nan_flags(q.x) | e4m3_nan_flags(q.y) | e4m3_nan_flags(q.z) | e4m3_nan_flags(q.w);
+                }
+                if (any == 0) continue;
+#pragma unroll 1
+                for (uint32_t e = 0; e < 64 && 64 * half + e < p.c.head_dim; ++e) {
+                    const uint32_t d = 64 * half + e;
+                    if ((codes[d] & 0x7F) != 0x7F || (marked[half] >> e & 1u)) continue;
+                    marked[half] |= 1ull << e;
+                    if (dst) dst[d] = 0x7FC0u;   // a NaN in BF16 and in FP16
+                    else part[d * stride] = __uint_as_float(0x7FC00000u);
+                }
             }
+        }
     }
 }
 // kPrefix: the CTAs that take part where the suffix pass runs beside this one: by the time of a unit here (256 rows, 128
@@ -491,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             sh_blocks.most = 0;
             tl->abort_flag = 0;
             tl->nan_seen = 0;
+            for (uint32_t i = 0; MODE != kFull && i < kNanWords; ++i) tl->nan_groups[i] = 0;
             fence_barrier_init();
         }
         __syncwarp();
@@ -817,9 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     }
                     if constexpr (MODE != kFull) {
                         if (*static_cast<volatile int*>(&tl->nan_seen) != 0 && real)
-                            mark_nan_span<MODE>(p, it.b, it.h, span, static_cast<int>(j0 * 8), static_cast<int>((j0 + cnt) * 8), row_end,
-                                          whole && put == nullptr ? dst : nullptr, put != nullptr ? put : slot + t * kTile + row,
-                                          put != nullptr ? 1u : kItemRows);
+                            mark_nan_span<MODE>(p, tl, unit0, static_cast<uint32_t>(u_end - u0), it.b, it.h, span, j0, cnt, row_end,
+                                                whole && put == nullptr ? dst : nullptr, put != nullptr ? put : slot + t * kTile + row,
+                                                put != nullptr ? 1u : kItemRows);
                     } else if (*static_cast<volatile int*>(&tl->nan_seen) != 0 && real)
                         mark_nan(p, it.b, it.h,
                                  max(static_cast<int>(j0 * kTile), edge_key(it.s, p.group, it.rb) / static_cast<int>(kTile) * static_cast<int>(kTile)),
@@ -1070,7 +1104,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                         for (uint32_t k = 0; k < CH; ++k) nan |= e4m3_nan_flags(vq[k].x) | e4m3_nan_flags(vq[k].y) | e4m3_nan_flags(vq[k].z) | e4m3_nan_flags(vq[k].w);
                         edge = edge && nan != 0u;
                     }
-                    if (edge) clean_tile(smem + C::kV + st * C::kTileBytes + st0, smem + C::kV + st * C::kTileBytes + st1, CH, kHalves, C::kHalfBytes, tl);
+                    if (edge) {
+                        uint8_t* const even = smem + C::kV + st * C::kTileBytes + st0;
+                        uint8_t* const odd = smem + C::kV + st * C::kTileBytes + st1;
+                        if constexpr (MODE != kFull) clean_tile<true>(even, odd, CH, kHalves, C::kHalfBytes, tl, 8 * i + 2 * cw, units);
+                        else clean_tile<false>(even, odd, CH, kHalves, C::kHalfBytes, tl);
+                    }
                     signal(&tl->vfull[st]);
                 }
                 if (more) load_codes(p.c.v_codes, vq);
