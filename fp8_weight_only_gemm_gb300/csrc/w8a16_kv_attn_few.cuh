@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
             tile_min = before + static_cast<int>(token_of(p, row0));
         Groups span{};
         int lo_max = 0;   // where the last row's window begins
+        int tile_max = 0;   // kPrefix: keys that some row sees
         if constexpr (MODE != kFull) {
             if (MODE == kPrefix) tile_end = p.span.lower;
             span = groups_of<MODE>(p, tile_min, tile_end);
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
                 if (MODE == kPrefix) {
                     end = real ? prefix_row_end(p, token_of(p, row)) : 0x7FFFFFFF;
                     tile_min = min(t == 0 ? 0x7FFFFFFF : tile_min, static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, end)));
+                    tile_max = max(tile_max, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, real ? end : 0)));
                 }
             }
             const float mine = bad && end <= 0 ? 0.f : rs.scale;
@@ -497,6 +499,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, NR>::kCtasPerSm)) kv_attn_k
                 break;
             }
             if ((step & 31u) == 0u) {   // the batch of 32 that the copies have reached
+                // Pages that no row of the tile sees: all rows may end before them, and nothing need have been written there yet. A masked
+                // score has no weight, but with a scale that is not finite.
+                if (MODE == kPrefix && key_of(step + lane) >= tile_max) meta_k = meta_v = 1.f;
                 cur_k = meta_k < kMinScale ? kMinScale : meta_k;
                 const float v = meta_v < kMinScale ? kMinScale : meta_v;
                 cur_lv = __log2f(v);

@@ -459,32 +459,41 @@ constexpr uint32_t kUnitCost = 8, kOwnItem = 4;
 __device__ __forceinline__ bool seq_is_ragged(const AttnArgs& p, const Seq& s) {
     return s.count > 0 && s.len > 0 && max(s.len - s.count, 0) + 1 < p.span.lower;
 }
-__device__ __noinline__ uint32_t prefix_share(const AttnArgs& p, uint64_t* sh, bool& ragged) {
+// seen: keys that some row sees, at most.
+__device__ __forceinline__ int seq_end(const Seq& s) { return s.count > 0 ? s.len : 0; }
+__device__ __noinline__ uint32_t prefix_share(const AttnArgs& p, uint64_t* sh, bool& ragged, int& seen) {
     const uint32_t rows = p.span.rows.max_q * p.group <= 8 ? 8u : 16u;
     uint64_t n = 0;
     bool any = false;
+    int end = 0;
     for (uint32_t b = threadIdx.x; b < p.span.rows.batch; b += blockDim.x) {
         const Seq s = sequence(p.span.rows, p.c.page_size, b);
         any = any || seq_is_ragged(p, s);
+        end = max(end, seq_end(s));
         if (s.len > p.span.lower)
             n += static_cast<uint64_t>((static_cast<uint32_t>(s.count) * p.group + rows - 1) / rows) * ((s.len - p.span.lower + 63) / 64 + kOwnItem);
     }
     n = warp_sum(n);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
+    end = __reduce_max_sync(0xFFFFFFFFu, end);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n, sh[kWarpsAll + (threadIdx.x >> 5)] = end;
     ragged = __syncthreads_or(any) != 0;
     n = 0;
-    for (uint32_t w = 0; w < kWarpsAll; ++w) n += sh[w];
+    for (uint32_t w = 0; w < kWarpsAll; ++w) n += sh[w], end = max(end, static_cast<int>(sh[kWarpsAll + w]));
+    seen = end;
     const uint64_t here = p.span.pass.total * kUnitCost, share = divide(here * p.ctas, here + n * p.c.kv_heads);
     return PrefixPass::even(min(static_cast<uint64_t>(p.span.pass.ctas), max(share, static_cast<uint64_t>(p.ctas / 4))),
                             static_cast<uint64_t>(p.span.pass.tiles) * p.c.kv_heads);
 }
 // kPrefix: whether a row that sees keys at all sees fewer than the prefix holds; for a warp.
-__device__ __noinline__ bool prefix_is_ragged(const AttnArgs& p) {
+__device__ __noinline__ bool prefix_is_ragged(const AttnArgs& p, int& seen) {
     bool ragged = false;
+    seen = 0;
     for (uint32_t b = threadIdx.x & 31; b < p.span.rows.batch; b += 32) {
         const Seq s = sequence(p.span.rows, p.c.page_size, b);
         ragged = ragged || seq_is_ragged(p, s);
+        seen = max(seen, seq_end(s));
     }
+    seen = __reduce_max_sync(0xFFFFFFFFu, seen);
     return __any_sync(0xFFFFFFFFu, ragged) != 0;
 }
 
@@ -543,11 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
     zero_keyless<MODE>(p);
     uint64_t ctas = active_ctas(total, p.ctas);
     bool ragged = false;
+    int seen = 0;
     if constexpr (MODE == kPrefix) {
         ctas = p.span.pass.ctas;
         grid_launch_dependents();   // a suffix pass runs beside this one, on the SMs that are left
         if (p.span.pass.taken != nullptr) {
-            ctas = prefix_share(p, sh_units, ragged);
+            ctas = prefix_share(p, sh_units, ragged, seen);
             if (blockIdx.x == 0 && threadIdx.x == 0) *p.span.pass.taken = static_cast<uint32_t>(ctas);
         }
     }
@@ -960,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
             const uint32_t q = lane / 8, g = lane % 8;
             // The item's keys: it_end; the units with keys that some row does not see: from it_edge on and, but for kFull, below it_lo.
             // There it_end, it_edge and it_lo are in the order of its groups, of which the first it_head come without it_skip.
-            if (MODE == kPrefix && p.span.pass.taken == nullptr) ragged = prefix_is_ragged(p);
+            if (MODE == kPrefix && p.span.pass.taken == nullptr) ragged = prefix_is_ragged(p, seen);
             int it_end = 0, it_edge = 0, it_lo = 0, it_head = 0, it_skip = 0;
             const auto enter = [&] {
                 it_end = block_end(it.s, p.group, it.rb);
@@ -1018,6 +1028,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     if (sk < kMinScale) sk = kMinScale;
                     if (sv < kMinScale) sv = kMinScale;
                 }
+                // (past all rows' ends, where nothing need have been written: masked scores have no weight, but with a scale that is not finite)
+                if (MODE == kPrefix && key >= seen) sk = sv = 1.f;
                 for (uint32_t k = 0; k < n && ok; ++k)
                     ok = wait_warp(smem_u32(&tl->lempty[(i + k) % kRing]), (((i + k) / kRing) & 1) ^ 1, tmo, abort_flag, kWaitLookFree);
                 if (!ok) break;
