@@ -21,8 +21,10 @@
 // tokens, 64 query heads) are 4.9 TB/s. A thread's query elements are asked for before the token's
 // position is known: with one task a thread, found by 64-bit divisions, and asked for after it,
 // that took 33 us; four tasks a thread take 31.6. Several axes: a token's positions are one more load in that chain
-// (one sequence, one token: 3.4 us a call for 3.1), and 4 sequences of 1369 tokens take 29.6 us for one axis's 25.5, with the axes in blocks
-// of pairs 27.0.
+// (one sequence, one token: 3.6 us a call for 2.9), and 4 sequences of 1369 tokens take 29.6 us for one axis's 25.5, the axes dealt in turn
+// or in blocks that end inside a chunk; in blocks of whole chunks 27.0. Large pages and few heads are far from memory's time: an item is a page of a
+// head for 128 threads, each with several tasks that it rotates twice (2 sequences of 149 tokens, pages of 128: 17.3 us for 13.5 MB; 2
+// of 1351, 8 heads of 64: 12.6 for 14.6).
 #include <cuda_runtime.h>
 
 #include <cstring>

@@ -13,7 +13,9 @@ namespace {
 
 // Whether the sequences' own keys behind a prefix go to the kernel for many rows. The one for few runs beside the prefix pass. us, few and
 // many, 8 heads of 128: 4 sequences of 12 tokens (48 rows a head), 600 keys behind 3000, 24 and 95; 16 of them, 700 behind 1000, 57 and 64; 2 of 16
-// (64), 2000 behind 3000, 33 and 52; 16 of them, 2000 behind 500, 95 and 90; 16 of 32 (128), 700 behind 1000, 125 and 58.
+// (64), 2000 behind 3000, 33 and 52; 16 of them, 2000 behind 500, 95 and 90; 16 of 32 (128), 700 behind 1000, 125 and 58. The host knows
+// rows, not lengths: where sequences with 33 to 64 rows a head have long keys of their own behind a short prefix this is the slower side
+// (32 of 16 tokens, 7500 behind 512: 549, and 248 without a shared prefix; 16, 2000 behind 500: 109 and 63).
 constexpr uint32_t kSuffixFewRows = 64;
 bool suffix_tc_applies(uint32_t head_dim, uint32_t rows_per_head) { return rows_per_head > kSuffixFewRows && kv_attn_tc_applies(head_dim, rows_per_head); }
 // Parts of a prefix item that it adds to its rows by itself; more are joined by a launch in between, on all SMs: an item's rows

@@ -771,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                     float* slot = slots + (static_cast<uint64_t>(blockIdx.x) * 2 + (first_part ? 0 : 1)) * ((DP + 2) * kItemRows);
                     const bool none = l == 0.f;   // a row that sees no key is zero
                     const float inv = none ? 0.f : 1.f / l;
-                    bool add = false;    // kSuffix: the row's parts of the prefix pass are still to be added
                     float* put = nullptr;   // kPrefix: the row's record, or its place in this CTA's slot
                     if constexpr (MODE != kFull) {
                         if (MODE == kPrefix) {
@@ -784,7 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tc_kernel(const AttnArgs 
                                 *reinterpret_cast<float2*>(record_max(p, p.span.record, at, DP)) = make_float2(ref, l);
                             }
                         }
-                        add = whole && real && MODE == kSuffix;
                     }
                     uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + static_cast<int64_t>(it.s.first + static_cast<int>(tok)) * p.out.token_stride +
                                     static_cast<int64_t>(head) * p.out.head_stride;

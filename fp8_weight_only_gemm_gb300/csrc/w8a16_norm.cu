@@ -11,10 +11,11 @@
 // y comes from h before its rounding. A group of 128 is 16 lanes' vectors, so its maximum is four shuffles.
 // A row's sums cross its warps through shared memory, one barrier a sum.
 //
-// Bound by: many rows, by HBM: 8192 of 8192 with both norms take 89 us, 6.0 TB/s, 90 % of a copy's rate (96 with an element at a
-// time: 64 % of issue slots). Rows brought into a ring ahead of a block that goes through them took 138: blocks of a row each have
-// more rows under way. Short and quantised rows stay further from it (4096 of 4096 with both norms 27 us, 5.0 TB/s; 4096 of 5120 with
-// an FP32 residual, quantised, 52, 4.4): their sums' barriers. One token of 4096: 1.7 us, the launch and one chain of loads and sums.
+// Bound by: many rows, by HBM: 8192 of 8192 with both norms take 92 us, 5.8 TB/s, 87 % of a copy's rate. Rows brought into a ring
+// ahead of a block that goes through them took 138: blocks of a row each have more rows under way. Fewer, shorter and quantised rows
+// stay further from it (4096 of 4096 with both norms 25.5 us, 79 %; 4096 of 5120 with an FP32 residual, quantised, 52.7, 66 %; 1974 of 4048, two
+// layer norms, 21, 46 %; 2145 of 1672, the same, 9.6, 34 %): a block holds one row, and no load runs under the barriers of its sums, two for a
+// layer norm. One token of 4096: 1.8 us, the launch and one chain of loads and sums.
 #include <cuda_runtime.h>
 
 #include <cstring>

@@ -479,6 +479,8 @@ typedef struct {
  *            sequence's own page table serves the positions from prefix_len on (also on the page that
  *            the prefix ends in), and its entries for pages that lie wholly below are not read. Sequences may be
  *            shorter than the prefix.
+ *            It is worth its passes where the prefix is long against what follows it: a sequence with up to 64 rows
+ *            a key/value head reads its own keys once for each 16 of them.
  * Not both. Rounding, padding, NaN and errors are as w8a16_kv_attention's, but the two passes of a prefix are
  * joined in FP32. Workspace: w8a16_kv_attention_ex_workspace_bytes(...). Two launches, with a prefix three
  * or four. */
