@@ -752,8 +752,8 @@ def kv_attention(cache, q, page_table, lens, out=None, *, softmax_scale=None, cu
     ones; pages that no query of the call sees a key of are not read, nor are their entries of
     page_table. prefix_pages, int32 [pages], with prefix_len: the first prefix_len positions of
     every sequence lie on these pages and are read once for all of them; page_table is
-    read for the positions behind. (Where those are many more than the prefix, a call with
-    page_table alone is the faster one.) Not both (w8a16_kv_attention_ex)."""
+    read for the positions behind. (Where those are many more than the prefix, a call without,
+    whose page_table names all pages, is the faster one.) Not both (w8a16_kv_attention_ex)."""
     if out is None:
         out = _new(stream, q.shape, q.dtype, q.device)
     if workspace is None:

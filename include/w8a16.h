@@ -441,7 +441,8 @@ W8A16_API int w8a16_kv_append_axes(const w8a16_kv_cache_t *cache, const w8a16_kv
  * Scales may be any positive FP32 values (those below 2^-60 count as 2^-60). Both
  * products take FP16 operands with FP32 sums: the E4M3 codes are exact, a query is
  * exact down to 2^-21 of its head's largest element, and the softmax weights are
- * rounded once to 11 bits. Queries without a visible key (lens[b] = 0, padding) give
+ * rounded once to 11 bits (fewer below 2^-21 of a row's largest, counted with the keys' value
+ * scales; those below 2^-32 count as 0). Queries without a visible key (lens[b] = 0, padding) give
  * zeros, whatever they hold; other queries with a non-finite element give NaN; what lies in slots past a
  * query's position has no effect, whatever its bits.
  *   workspace  device memory, 16-byte aligned, at least
